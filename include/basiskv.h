@@ -17,6 +17,14 @@
  *                        Value latents (rank-r output per head)
  *   basiskv_out_proj     (step 5)   y = sum_h o_h G_h through the fused factor
  *
+ * Around the step: basiskv_assign_pages / basiskv_release_pages keep the block
+ * table of requests that grow or end, basiskv_rotary turns the new queries and
+ * keys by their positions before they are appended and attend, and
+ * basiskv_dense_attn attends over the whole cache (one new token or many per
+ * sequence; capped scores, distance bias, window and prefix masks) where a
+ * layer, or a prompt, is not routed.  Its o_lat goes to basiskv_out_proj like
+ * step 4's.
+ *
  * basiskv_append_route does steps 1-3 in one call, the route's scoring running
  * beside the append (no second stream needed).  A step whose inputs and output
  * live in page-locked host memory brings the inputs in with basiskv_copy and
@@ -67,7 +75,9 @@ extern "C" {
 
 /* 1: append, route, decode_attn, out_proj and their helpers;
  * 2: adds basiskv_route_group and basiskv_prefill;
- * 3: decode_attn accepts sel = sel_cnt = NULL (the routing call's selection). */
+ * 3: decode_attn accepts sel = sel_cnt = NULL (the routing call's selection);
+ * 4: basiskv_copy, basiskv_append_route, y in host memory.  Calls added since
+ * (pages, rotary, dense_attn) left the existing ones as they were. */
 #define BASISKV_ABI_VERSION 4
 
 typedef enum {
@@ -89,6 +99,7 @@ typedef enum { BASISKV_GROUP_SUM = 1, BASISKV_GROUP_MAX = 2 } basiskv_group_redu
 #define BASISKV_DEVERR_SEQ_LEN 4       /* seq_len < n_new, or > max_pages * page_size         */
 #define BASISKV_DEVERR_TIMEOUT 8       /* an in-kernel wait on a bulk copy gave up (~1 s)     */
 #define BASISKV_DEVERR_WORKSPACE 16    /* a workspace counter was not zero: not zero-filled   */
+#define BASISKV_DEVERR_PAGES 32        /* free pages fewer than a call needs, or more than exist */
 
 /*
  * Shapes.  Supported by this build: head_dim in {64, 128}; page_size in
@@ -356,6 +367,169 @@ BASISKV_API basiskv_status basiskv_fuse_out_factor(const basiskv_config* cfg, co
  * stream has passed the copy.  bytes = 0 does nothing.
  */
 BASISKV_API basiskv_status basiskv_copy(void* dst, const void* src, size_t bytes, void* stream);
+
+/*
+ * Pages for requests that grow.  Request b holds seq_len[b] tokens and gets
+ * add_len[b] more (zero included): with have = ceil(seq_len / P) and
+ * want = ceil((seq_len + add_len) / P), entries have .. want - 1 of its
+ * block_table row are set to pages taken from the free list, whose valid
+ * entries are free_pages[0 .. *free_count - 1]: the pages of all requests, in
+ * request order, are free_pages[*free_count - 1], free_pages[*free_count - 2]
+ * and so on.  Other entries of the table are left as they are.
+ *   seq_len_out [batch]   seq_len + add_len (basiskv_append's seq_len)
+ *   free_count_out        *free_count less the pages taken
+ *   slots [batch][slot_cols] (optional, may be NULL)  for the first slot_cols
+ *     new tokens t of request b the token's slot, physical page * P +
+ *     position % P with position seq_len[b] + t; -1 for t >= add_len[b]
+ * seq_len_out may be seq_len and free_count_out may be free_count (a step in
+ * place); no other two arguments may overlap.  block_table is
+ * [batch][max_pages].  All arrays int32 (device).
+ * A call that cannot be met changes nothing but its outputs' copies
+ * (seq_len_out = seq_len, free_count_out = free_count, slots all -1) and sets
+ * *err_flag: BASISKV_DEVERR_SEQ_LEN for a negative length or more pages than a
+ * table row holds, BASISKV_DEVERR_PAGES for too few free pages or a count
+ * outside [0, num_phys_pages], BASISKV_DEVERR_BLOCK_TABLE for a page id outside
+ * [0, num_phys_pages) in the part of the free list, or the partly filled last
+ * page, that it would hand on.
+ * Of cfg only page_size is used (all of it is checked).  batch at most 16384
+ * (else BASISKV_ERR_UNSUPPORTED).
+ */
+BASISKV_API basiskv_status basiskv_assign_pages(const basiskv_config* cfg, int32_t batch, int32_t max_pages,
+                                                int32_t num_phys_pages, const int32_t* seq_len,
+                                                const int32_t* add_len, int32_t* block_table,
+                                                const int32_t* free_pages, const int32_t* free_count,
+                                                int32_t* seq_len_out, int32_t* free_count_out, int32_t* slots,
+                                                int32_t slot_cols, int32_t* err_flag, void* stream);
+
+/*
+ * Pages of requests that end.  The ceil(seq_len[b] / P) pages of every request
+ * with release[b] != 0 go back to the free list: page i of request b to
+ * free_pages[*free_count + i + pages of the released requests before b]
+ * (free_pages holds num_phys_pages entries).  seq_len_out[b] is 0 for a
+ * released request and seq_len[b] for the others; free_count_out counts the
+ * pages.  block_table is not changed (an entry past a sequence's pages is never
+ * read).  In-place use, faults (a page id outside the pool, more free pages than
+ * the pool holds, a bad length: nothing is released) and limits as for
+ * basiskv_assign_pages.
+ */
+BASISKV_API basiskv_status basiskv_release_pages(const basiskv_config* cfg, int32_t batch, int32_t max_pages,
+                                                 int32_t num_phys_pages, const int32_t* seq_len,
+                                                 const int32_t* release, const int32_t* block_table,
+                                                 int32_t* free_pages, const int32_t* free_count,
+                                                 int32_t* seq_len_out, int32_t* free_count_out, int32_t* err_flag,
+                                                 void* stream);
+
+/* Which two elements of a head make pair i of its first rotary_dim elements. */
+typedef enum {
+  BASISKV_ROPE_HALF = 0,        /* (i, i + rotary_dim / 2) */
+  BASISKV_ROPE_INTERLEAVED = 1  /* (2 i, 2 i + 1)          */
+} basiskv_rope_layout;
+
+/* How the frequencies are scaled for contexts longer than they were made for. */
+typedef enum {
+  BASISKV_ROPE_NONE = 0,   /* f_i = base^(-2 i / rotary_dim)                                     */
+  BASISKV_ROPE_LINEAR = 1, /* f_i / factor                                                       */
+  BASISKV_ROPE_NTK = 2,    /* base * factor^(rotary_dim / (rotary_dim - 2)) in place of base     */
+  BASISKV_ROPE_YARN = 3,   /* f_i (1 - ramp_i) + f_i / factor * ramp_i, ramp_i rising from 0 to 1
+                              between the pairs that make beta_fast and beta_slow turns over
+                              original_len (rounded outwards to whole pairs); cos and sin times
+                              0.1 ln(factor) + 1 (factor > 1)                                   */
+  BASISKV_ROPE_LLAMA3 = 4  /* f_i / factor where the wavelength is above original_len /
+                              low_freq_factor, f_i where below original_len / high_freq_factor,
+                              between them linear in original_len / wavelength                  */
+} basiskv_rope_scaling;
+
+typedef struct {
+  int32_t layout;       /* basiskv_rope_layout                                        */
+  int32_t rotary_dim;   /* even, 2 .. 128: elements of each head that are rotated     */
+  int32_t scaling;      /* basiskv_rope_scaling                                       */
+  double base;          /* > 1                                                        */
+  double factor;        /* >= 1 (read where the scaling uses it, like what follows)   */
+  double original_len;  /* > 0                                                        */
+  double beta_fast, beta_slow;             /* yarn: beta_fast > beta_slow > 0         */
+  double low_freq_factor, high_freq_factor; /* llama3: high > low > 0                 */
+} basiskv_rope_params;
+
+/* The rotation as the kernels take it (host memory, written by basiskv_rope_init). */
+typedef struct {
+  int32_t layout, rotary_dim;
+  float mscale;         /* factor on cos and sin                                      */
+  int32_t reserved;
+  double inv_freq[64];  /* radians per position of each pair                          */
+} basiskv_rope;
+
+/* Fills `rope` (host) from `params`; once per model, not per step. */
+BASISKV_API basiskv_status basiskv_rope_init(basiskv_rope* rope, const basiskv_rope_params* params);
+
+/*
+ * Rotary positions of new queries and keys, before basiskv_append (or
+ * basiskv_prefill) stores the keys and the queries attend: pair (u, v) of the
+ * token at position x becomes (u cos - v sin, v cos + u sin) * mscale with the
+ * angle x * inv_freq_i; elements from rotary_dim on are copied.
+ *   q [batch][n_new] tokens of [Hq][d], q_stride elements from one token to the
+ *     next (>= Hq * d: a row of a fused projection's output is such a stride);
+ *     q_out dense [batch][n_new][Hq][d]; the same for k with Hkv (dtype, device).
+ *     Either of q and k may be NULL (with its output).  q_out may be q where
+ *     q_stride is Hq * d, k_out likewise; other overlaps are not allowed.
+ *   positions (device) [batch][n_new] int32, or NULL: token t of sequence b is
+ *     at seq_len[b] - n_new + t, as basiskv_append places it (seq_len (device)
+ *     [batch]).  Exactly one of the two is given.
+ * The angle is formed and reduced in fp64, sin and cos and the products are
+ * fp32, the result is rounded once to dtype.
+ */
+BASISKV_API basiskv_status basiskv_rotary(const basiskv_config* cfg, const basiskv_rope* rope, const void* q,
+                                          int64_t q_stride, const void* k, int64_t k_stride, void* q_out,
+                                          void* k_out, const int32_t* positions, const int32_t* seq_len,
+                                          int32_t batch, int32_t n_new, void* stream);
+
+/* What a layer's scores are besides scaled dot products.  NULL in place of a
+ * pointer to it: the defaults (all zero). */
+typedef struct {
+  float scale;               /* 0: 1 / sqrt(head_dim); else > 0                        */
+  float softcap;             /* c > 0: scores become c tanh(s / c); 0: not capped      */
+  int32_t window;            /* w > 0: a token sees the last w tokens, itself included */
+  int32_t reserved;
+  const float* slopes;       /* (device) [Hq]: slope_h * |i - j| is taken off the score
+                                of query position i and key position j; NULL: no bias  */
+  const int32_t* prefix_len; /* (device) [batch]: every new token sees the first
+                                prefix_len[b] tokens, later ones among them too and
+                                whatever the window (clamped to 0 .. seq_len); NULL: 0 */
+} basiskv_attn_options;
+
+/*
+ * Attention of the last n_new tokens of every sequence over its whole paged
+ * cache (they are in it: basiskv_append or basiskv_prefill came before).
+ * q (device, dtype) [batch][n_new][Hq][d]; token t of sequence b is at position
+ * i = seq_len[b] - n_new + t and sees key j < seq_len[b] if j <= i (and
+ * i - j < window, where there is one) or j < prefix_len[b].  With
+ * s_j = scale q_h . K_j, capped, then less the bias, w = softmax(s):
+ *   o_lat [batch][n_new][Hq][r] (fp32)  sum_j w_j C_j
+ *   lse   [batch][n_new][Hq]    (fp32, optional, may be NULL)  ln sum_j exp(s_j),
+ *         by which results over parts of a context can be joined
+ * A row that sees nothing has o_lat 0 and lse -inf; so do all rows of a
+ * sequence with seq_len[b] = 0 (a padded batch), which is no error.  A length
+ * below n_new or above max_pages * P sets BASISKV_DEVERR_SEQ_LEN and its rows
+ * are as if it were 0.  A block-table entry out of range sets
+ * BASISKV_DEVERR_BLOCK_TABLE and its tokens are not seen; entries of pages that
+ * no new token sees (past the sequence, before every window) are not read.
+ * Latents of tokens that some new token of the call sees must be finite (a
+ * weight of zero does not stop a NaN); any bits may stand elsewhere.
+ * Scores, softmax and sums are fp32; a bf16 cache's weights are multiplied as
+ * bf16 pairs (hi + lo, 16 mantissa bits).  Repeated calls on the same inputs
+ * give bitwise identical results.
+ * cache->r_res and cache->summary are not read (they may be NULL).
+ * workspace (device): basiskv_dense_attn_workspace_bytes bytes, zero-filled
+ * once when it is allocated, and again before it serves another shape; calls
+ * that share one must not overlap.  batch at most 65535.
+ */
+BASISKV_API basiskv_status basiskv_dense_attn(const basiskv_config* cfg, const basiskv_cache* cache, const void* q,
+                                              int32_t batch, int32_t n_new, const basiskv_attn_options* options,
+                                              float* o_lat, float* lse, void* workspace, size_t workspace_bytes,
+                                              int32_t* err_flag, void* stream);
+
+/* Workspace bytes basiskv_dense_attn needs for this shape (0 for a bad one). */
+BASISKV_API size_t basiskv_dense_attn_workspace_bytes(const basiskv_config* cfg, int32_t batch, int32_t n_new,
+                                                      int32_t max_pages);
 
 /* Workspace bytes needed by route / decode_attn / out_proj for this shape. */
 BASISKV_API size_t basiskv_workspace_bytes(const basiskv_config* cfg, int32_t batch, int32_t max_pages);

@@ -21,13 +21,17 @@ OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_WORKSPACE = 0, 1, 2, 3, 4
 F32, BF16 = 0, 1
 GROUP_SUM, GROUP_MAX = 1, 2
 DEVERR_BLOCK_TABLE, DEVERR_SELECTION, DEVERR_SEQ_LEN, DEVERR_TIMEOUT, DEVERR_WORKSPACE = 1, 2, 4, 8, 16
+DEVERR_PAGES = 32
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "llama3": 4}
 
 # every function include/basiskv.h declares
 SYMBOLS = [
     "basiskv_append", "basiskv_route", "basiskv_decode_attn", "basiskv_out_proj",
     "basiskv_fuse_out_factor", "basiskv_workspace_bytes", "basiskv_status_string",
     "basiskv_abi_version", "basiskv_decode_attn_noalloc", "basiskv_route_group", "basiskv_prefill",
-    "basiskv_copy", "basiskv_append_route",
+    "basiskv_copy", "basiskv_append_route", "basiskv_assign_pages", "basiskv_release_pages",
+    "basiskv_rope_init", "basiskv_rotary", "basiskv_dense_attn", "basiskv_dense_attn_workspace_bytes",
 ]
 
 
@@ -47,6 +51,22 @@ class CCache(ctypes.Structure):
 class CFactors(ctypes.Structure):
     _fields_ = [("A", ctypes.c_void_p), ("P", ctypes.c_void_p), ("E", ctypes.c_void_p),
                 ("Gt", ctypes.c_void_p)]
+
+
+class CRopeParams(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ["layout", "rotary_dim", "scaling"]]
+                + [(n, ctypes.c_double) for n in ["base", "factor", "original_len", "beta_fast", "beta_slow",
+                                                  "low_freq_factor", "high_freq_factor"]])
+
+
+class CRope(ctypes.Structure):
+    _fields_ = [("layout", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("mscale", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("inv_freq", ctypes.c_double * 64)]
+
+
+class CAttnOptions(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("window", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("slopes", ctypes.c_void_p), ("prefix_len", ctypes.c_void_p)]
 
 
 _lib = None
@@ -73,6 +93,14 @@ def lib():
     L.basiskv_fuse_out_factor.argtypes = [pc, vp, vp, vp, vp]
     L.basiskv_copy.argtypes = [vp, vp, sz, vp]
     L.basiskv_append_route.argtypes = [pc, pk, pf, vp, vp, vp, i32, i32, vp, vp, vp, sz, vp, vp]
+    i64, pr, pa = ctypes.c_int64, ctypes.POINTER(CRope), ctypes.POINTER(CAttnOptions)
+    L.basiskv_assign_pages.argtypes = [pc, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, vp]
+    L.basiskv_release_pages.argtypes = [pc, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.basiskv_rope_init.argtypes = [pr, ctypes.POINTER(CRopeParams)]
+    L.basiskv_rotary.argtypes = [pc, pr, vp, i64, vp, i64, vp, vp, vp, vp, i32, i32, vp]
+    L.basiskv_dense_attn.argtypes = [pc, pk, vp, i32, i32, pa, vp, vp, vp, sz, vp, vp]
+    L.basiskv_dense_attn_workspace_bytes.argtypes = [pc, i32, i32, i32]
+    L.basiskv_dense_attn_workspace_bytes.restype = sz
     L.basiskv_workspace_bytes.argtypes = [pc, i32, i32]
     L.basiskv_workspace_bytes.restype = sz
     L.basiskv_status_string.argtypes = [i32]
@@ -80,7 +108,9 @@ def lib():
     L.basiskv_abi_version.argtypes = []
     for name in ["basiskv_append", "basiskv_route", "basiskv_decode_attn", "basiskv_out_proj",
                  "basiskv_fuse_out_factor", "basiskv_abi_version", "basiskv_decode_attn_noalloc",
-                 "basiskv_route_group", "basiskv_prefill", "basiskv_copy", "basiskv_append_route"]:
+                 "basiskv_route_group", "basiskv_prefill", "basiskv_copy", "basiskv_append_route",
+                 "basiskv_assign_pages", "basiskv_release_pages", "basiskv_rope_init", "basiskv_rotary",
+                 "basiskv_dense_attn"]:
         getattr(L, name).restype = i32
     _lib = L
     return L
@@ -345,3 +375,199 @@ def decode_attn_noalloc(cfg: Config, cache: PagedCache, q: torch.Tensor, sel: to
     _check(lib().basiskv_decode_attn_noalloc(ctypes.byref(cfg.c()), ctypes.byref(cache.c()), _ptr(q), B,
                                              _ptr(sel), _ptr(sel_cnt), _ptr(o_lat), _ptr(err),
                                              _stream(stream)), "basiskv_decode_attn_noalloc")
+
+
+def _same_device(first: torch.Tensor, **others):
+    """Every tensor on `first`'s device, which must be the current one (the kernels launch there)."""
+    if first.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {first.device}, the current device is cuda:{torch.cuda.current_device()}")
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, expected {first.device}")
+
+
+def assign_pages(cfg: Config, block_table: torch.Tensor, seq_len: torch.Tensor, add_len: torch.Tensor,
+                 free_pages: torch.Tensor, free_count: torch.Tensor, seq_len_out: torch.Tensor,
+                 free_count_out: torch.Tensor, slots: Optional[torch.Tensor], err: torch.Tensor, stream=None):
+    """Pages for add_len[b] new tokens of every request b: entries of block_table [B, max_pages] taken
+    from the free list (free_pages [num_phys], its first free_count[0] entries), seq_len_out = seq_len +
+    add_len, free_count_out, and (slots [B, cols], or None) the slot page * P + position % P of each new
+    token.  seq_len_out may be seq_len and free_count_out may be free_count (basiskv_assign_pages)."""
+    i32, B = torch.int32, seq_len.numel()
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [batch, max_pages]")
+    max_pages = block_table.shape[1]
+    _need(seq_len, "seq_len", i32, (B,))
+    _need(block_table, "block_table", i32, (B, max_pages))
+    _need(add_len, "add_len", i32, (B,))
+    _need(free_pages, "free_pages", i32, (free_pages.numel(),))
+    _need(free_count, "free_count", i32, (1,))
+    _need(seq_len_out, "seq_len_out", i32, (B,))
+    _need(free_count_out, "free_count_out", i32, (1,))
+    _need(err, "err", i32)
+    if slots is not None:
+        _need(slots, "slots", i32, (B, slots.shape[1]) if slots.dim() == 2 else (B, -1))
+    _same_device(seq_len, block_table=block_table, add_len=add_len, free_pages=free_pages, free_count=free_count,
+                 seq_len_out=seq_len_out, free_count_out=free_count_out, slots=slots, err=err)
+    _check(lib().basiskv_assign_pages(ctypes.byref(cfg.c()), B, max_pages, free_pages.numel(), _ptr(seq_len),
+                                      _ptr(add_len), _ptr(block_table), _ptr(free_pages), _ptr(free_count),
+                                      _ptr(seq_len_out), _ptr(free_count_out), _ptr(slots),
+                                      0 if slots is None else slots.shape[1], _ptr(err), _stream(stream)),
+           "basiskv_assign_pages")
+
+
+def release_pages(cfg: Config, block_table: torch.Tensor, seq_len: torch.Tensor, release: torch.Tensor,
+                  free_pages: torch.Tensor, free_count: torch.Tensor, seq_len_out: torch.Tensor,
+                  free_count_out: torch.Tensor, err: torch.Tensor, stream=None):
+    """Back to the free list with the pages of every request whose release[b] is not zero;
+    seq_len_out is 0 for them (basiskv_release_pages)."""
+    i32, B = torch.int32, seq_len.numel()
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [batch, max_pages]")
+    max_pages = block_table.shape[1]
+    _need(seq_len, "seq_len", i32, (B,))
+    _need(block_table, "block_table", i32, (B, max_pages))
+    _need(release, "release", i32, (B,))
+    _need(free_pages, "free_pages", i32, (free_pages.numel(),))
+    _need(free_count, "free_count", i32, (1,))
+    _need(seq_len_out, "seq_len_out", i32, (B,))
+    _need(free_count_out, "free_count_out", i32, (1,))
+    _need(err, "err", i32)
+    _same_device(seq_len, block_table=block_table, release=release, free_pages=free_pages, free_count=free_count,
+                 seq_len_out=seq_len_out, free_count_out=free_count_out, err=err)
+    _check(lib().basiskv_release_pages(ctypes.byref(cfg.c()), B, max_pages, free_pages.numel(), _ptr(seq_len),
+                                       _ptr(release), _ptr(block_table), _ptr(free_pages), _ptr(free_count),
+                                       _ptr(seq_len_out), _ptr(free_count_out), _ptr(err), _stream(stream)),
+           "basiskv_release_pages")
+
+
+class Rope:
+    """Rotary frequencies of a model (basiskv_rope_init), made once and passed to every rotary call.
+
+    layout: "half" (pair i is elements i and i + rotary_dim / 2) or "interleaved" (2i, 2i + 1);
+    rotary_dim: how much of each head is rotated (default: all of it);
+    scaling: "none", "linear", "ntk", "yarn" or "llama3" with their parameters."""
+
+    def __init__(self, cfg: Config, base: float = 10000.0, rotary_dim: Optional[int] = None, layout: str = "half",
+                 scaling: str = "none", factor: float = 1.0, original_len: float = 0.0, beta_fast: float = 32.0,
+                 beta_slow: float = 1.0, low_freq_factor: float = 1.0, high_freq_factor: float = 4.0):
+        if layout not in ROPE_LAYOUTS:
+            raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}, not {layout!r}")
+        if scaling not in ROPE_SCALINGS:
+            raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}, not {scaling!r}")
+        self.rotary_dim = cfg.head_dim if rotary_dim is None else int(rotary_dim)
+        if self.rotary_dim > cfg.head_dim:
+            raise ValueError(f"rotary_dim {self.rotary_dim} > head_dim {cfg.head_dim}")
+        self.c = CRope()
+        par = CRopeParams(ROPE_LAYOUTS[layout], self.rotary_dim, ROPE_SCALINGS[scaling], base, factor, original_len,
+                          beta_fast, beta_slow, low_freq_factor, high_freq_factor)
+        _check(lib().basiskv_rope_init(ctypes.byref(self.c), ctypes.byref(par)), "basiskv_rope_init")
+
+    @property
+    def inv_freq(self):
+        """Radians per position of each pair (a list)."""
+        return list(self.c.inv_freq)[:self.rotary_dim // 2]
+
+    @property
+    def mscale(self) -> float:
+        return float(self.c.mscale)
+
+
+def _token_stride(t: torch.Tensor, name: str, dtype, shape) -> int:
+    """Elements from one token of t [B, n, heads, d] to the next: dense heads, tokens evenly spaced
+    (a slice of a packed projection's heads is)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    B, n, h, d = shape
+    st = t.stride()
+    step = st[1] if n > 1 else st[0] if B > 1 else h * d
+    if (st[3] != 1 or (h > 1 and st[2] != d) or (B > 1 and n > 1 and st[0] != n * st[1]) or step < h * d):
+        raise ValueError(f"{name}: heads must be dense and tokens evenly spaced, strides are {st}")
+    return step
+
+
+def rotary(cfg: Config, rope: Rope, q: Optional[torch.Tensor], k: Optional[torch.Tensor],
+           q_out: Optional[torch.Tensor], k_out: Optional[torch.Tensor], seq_len: Optional[torch.Tensor] = None,
+           positions: Optional[torch.Tensor] = None, stream=None):
+    """q [B, n, Hq, d] and k [B, n, Hkv, d] (either may be None, with its output) rotated by their
+    tokens' positions into q_out and k_out, which may be q and k: positions [B, n], or seq_len [B], which
+    counts the n new tokens already (token t is at seq_len - n + t).  q and k may be head slices of one
+    packed projection [B, n, heads, d]; the outputs are dense (basiskv_rotary)."""
+    first = q if q is not None else k
+    if first is None:
+        raise ValueError("rotary: neither q nor k given")
+    B, n = first.shape[0], first.shape[1]
+    strides = [0, 0]
+    for x, (t, out, heads, name) in enumerate(((q, q_out, cfg.num_q_heads, "q"), (k, k_out, cfg.num_kv_heads, "k"))):
+        if (t is None) != (out is None):
+            raise ValueError(f"{name} and {name}_out are given together or not at all")
+        if t is not None:
+            shape = (B, n, heads, cfg.head_dim)
+            strides[x] = _token_stride(t, name, cfg.dtype, shape)
+            _need(out, name + "_out", cfg.dtype, shape)
+    if (positions is None) == (seq_len is None):
+        raise ValueError("give either positions or seq_len")
+    if positions is not None:
+        _need(positions, "positions", torch.int32, (B, n))
+    else:
+        _need(seq_len, "seq_len", torch.int32, (B,))
+    _same_device(first, q=q, k=k, q_out=q_out, k_out=k_out, positions=positions, seq_len=seq_len)
+    _check(lib().basiskv_rotary(ctypes.byref(cfg.c()), ctypes.byref(rope.c), _ptr(q), strides[0], _ptr(k), strides[1],
+                                _ptr(q_out), _ptr(k_out), _ptr(positions), _ptr(seq_len), B, n, _stream(stream)),
+           "basiskv_rotary")
+
+
+@dataclass
+class AttnOptions:
+    """What a layer's scores are besides scaled dot products (basiskv_attn_options)."""
+    scale: float = 0.0                          # 0: 1 / sqrt(head_dim)
+    softcap: float = 0.0                        # c > 0: c tanh(s / c)
+    window: int = 0                             # w > 0: the last w tokens, itself included
+    slopes: Optional[torch.Tensor] = None       # [Hq] fp32: slope * distance is taken off
+    prefix_len: Optional[torch.Tensor] = None   # [B] int32: tokens that every new token sees
+
+
+def dense_workspace_bytes(cfg: Config, batch: int, n_new: int, max_pages: int) -> int:
+    return int(lib().basiskv_dense_attn_workspace_bytes(ctypes.byref(cfg.c()), batch, n_new, max_pages))
+
+
+def alloc_dense_workspace(cfg: Config, batch: int, n_new: int, max_pages: int, device="cuda") -> torch.Tensor:
+    """A zero-filled workspace of dense_attn for one shape (its counters are left at zero between calls)."""
+    return torch.zeros(max(dense_workspace_bytes(cfg, batch, n_new, max_pages), 256), dtype=torch.uint8, device=device)
+
+
+def dense_attn(cfg: Config, cache: PagedCache, q: torch.Tensor, o_lat: torch.Tensor, ws: torch.Tensor,
+               err: torch.Tensor, options: Optional[AttnOptions] = None, lse: Optional[torch.Tensor] = None,
+               stream=None):
+    """Attention of the last n tokens of every sequence over its whole cache: q [B, n, Hq, d] ->
+    o_lat [B, n, Hq, r] and, where given, lse [B, n, Hq] (fp32).  Without the n axis (q [B, Hq, d]) one token
+    each.  ws from alloc_dense_workspace (basiskv_dense_attn)."""
+    if q.dim() not in (3, 4):
+        raise ValueError("q must be [B, n, Hq, d] or [B, Hq, d]")
+    lead = tuple(q.shape[:-2])
+    B, n = lead[0], lead[1] if len(lead) == 2 else 1
+    _need(q, "q", cfg.dtype, lead + (cfg.num_q_heads, cfg.head_dim))
+    _need(o_lat, "o_lat", torch.float32, lead + (cfg.num_q_heads, cfg.rank_v))
+    _need(ws, "workspace", torch.uint8)
+    _need(err, "err", torch.int32)
+    if B != cache.batch:
+        raise ValueError(f"q has {B} sequences, the cache {cache.batch}")
+    if lse is not None:
+        _need(lse, "lse", torch.float32, lead + (cfg.num_q_heads,))
+    opt, slopes, prefix = None, None, None
+    if options is not None:
+        slopes, prefix = options.slopes, options.prefix_len
+        if slopes is not None:
+            _need(slopes, "slopes", torch.float32, (cfg.num_q_heads,))
+        if prefix is not None:
+            _need(prefix, "prefix_len", torch.int32, (B,))
+        opt = ctypes.byref(CAttnOptions(options.scale, options.softcap, options.window, 0, _ptr(slopes), _ptr(prefix)))
+    _same_device(q, cache=cache.k_raw, o_lat=o_lat, workspace=ws, err=err, lse=lse, slopes=slopes, prefix_len=prefix)
+    _check(lib().basiskv_dense_attn(ctypes.byref(cfg.c()), ctypes.byref(cache.c()), _ptr(q), B, n, opt, _ptr(o_lat),
+                                    _ptr(lse), _ptr(ws), ws.numel(), _ptr(err), _stream(stream)), "basiskv_dense_attn")

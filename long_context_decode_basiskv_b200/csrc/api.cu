@@ -2,6 +2,9 @@
 // layout and kernel dispatch.  Nothing here allocates device memory.
 #include <stdio.h>
 
+#include <math.h>
+
+#include "dense_attn.cuh"
 #include "kernels.cuh"
 #include "union.cuh"
 
@@ -11,6 +14,8 @@ namespace bkv {
 // helpers
 // ---------------------------------------------------------------------------
 constexpr int kMaxPagesLimit = 49152;  // route select keeps one key per page in shared memory
+constexpr int kMaxRequests = 16384;    // the pages kernel keeps two words per request in shared memory
+constexpr int kMaxBatch = 65535;       // sequences of a dense_attn grid
 
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -303,6 +308,178 @@ basiskv_status basiskv_copy(void* dst, const void* src, size_t bytes, void* stre
   const uintptr_t a = reinterpret_cast<uintptr_t>(d), b = reinterpret_cast<uintptr_t>(s);
   if (a < b + bytes && b < a + bytes) return BASISKV_ERR_INVALID_ARG;  // overlapping ranges
   return cuda_status(launch_copy(d, s, bytes, num_sms(), (cudaStream_t)stream));
+}
+
+static basiskv_status pages_common(const basiskv_config* cfg, int32_t batch, int32_t max_pages, int32_t num_phys,
+                                   const int32_t* seq_len, const int32_t* amount, const int32_t* table,
+                                   const int32_t* free_pages, const int32_t* free_count, int32_t* seq_len_out,
+                                   int32_t* free_count_out, int32_t* slots, int32_t slot_cols, int32_t* err_flag,
+                                   PagesParams* p) {
+  basiskv_status s = check_config(cfg);
+  if (s != BASISKV_OK) return s;
+  if (batch < 0 || max_pages <= 0 || num_phys <= 0) return BASISKV_ERR_INVALID_ARG;
+  if (max_pages > kMaxPagesLimit || num_phys > kMaxPhysPages || batch > kMaxRequests) return BASISKV_ERR_UNSUPPORTED;
+  if (batch == 0) return BASISKV_OK;
+  if (!seq_len || !amount || !table || !free_pages || !free_count || !seq_len_out || !free_count_out || !err_flag)
+    return BASISKV_ERR_INVALID_ARG;
+  if (slots && slot_cols <= 0) return BASISKV_ERR_INVALID_ARG;
+  // in place: each output over its own input only
+  if (amount == seq_len_out || amount == free_count_out || seq_len == free_count_out || free_count == seq_len_out ||
+      seq_len_out == free_count_out)
+    return BASISKV_ERR_INVALID_ARG;
+  *p = PagesParams{seq_len, amount, const_cast<int32_t*>(table), const_cast<int32_t*>(free_pages), free_count,
+                   seq_len_out, free_count_out, slots, err_flag, batch, cfg->page_size, max_pages, num_phys,
+                   slot_cols, (slot_cols % 4 == 0 && aligned16(slots)) ? 4 : 1};
+  return BASISKV_OK;
+}
+
+basiskv_status basiskv_assign_pages(const basiskv_config* cfg, int32_t batch, int32_t max_pages, int32_t num_phys,
+                                    const int32_t* seq_len, const int32_t* add_len, int32_t* block_table,
+                                    const int32_t* free_pages, const int32_t* free_count, int32_t* seq_len_out,
+                                    int32_t* free_count_out, int32_t* slots, int32_t slot_cols, int32_t* err_flag,
+                                    void* stream) {
+  PagesParams p;
+  const basiskv_status s = pages_common(cfg, batch, max_pages, num_phys, seq_len, add_len, block_table, free_pages,
+                                        free_count, seq_len_out, free_count_out, slots, slot_cols, err_flag, &p);
+  if (s != BASISKV_OK || batch == 0) return s;
+  return cuda_status(launch_assign_pages(p, (cudaStream_t)stream));
+}
+
+basiskv_status basiskv_release_pages(const basiskv_config* cfg, int32_t batch, int32_t max_pages, int32_t num_phys,
+                                     const int32_t* seq_len, const int32_t* release, const int32_t* block_table,
+                                     int32_t* free_pages, const int32_t* free_count, int32_t* seq_len_out,
+                                     int32_t* free_count_out, int32_t* err_flag, void* stream) {
+  PagesParams p;
+  const basiskv_status s = pages_common(cfg, batch, max_pages, num_phys, seq_len, release, block_table, free_pages,
+                                        free_count, seq_len_out, free_count_out, nullptr, 0, err_flag, &p);
+  if (s != BASISKV_OK || batch == 0) return s;
+  return cuda_status(launch_release_pages(p, (cudaStream_t)stream));
+}
+
+basiskv_status basiskv_rope_init(basiskv_rope* rope, const basiskv_rope_params* a) {
+  if (!rope || !a) return BASISKV_ERR_INVALID_ARG;
+  auto positive = [](double x) { return x > 0.0 && isfinite(x); };
+  const int D = a->rotary_dim, kind = a->scaling;
+  if (a->layout != BASISKV_ROPE_HALF && a->layout != BASISKV_ROPE_INTERLEAVED) return BASISKV_ERR_INVALID_ARG;
+  if (D < 2 || D % 2 != 0 || D > 128) return BASISKV_ERR_INVALID_ARG;
+  if (kind < BASISKV_ROPE_NONE || kind > BASISKV_ROPE_LLAMA3) return BASISKV_ERR_INVALID_ARG;
+  if (!(a->base > 1.0) || !isfinite(a->base)) return BASISKV_ERR_INVALID_ARG;
+  if (kind != BASISKV_ROPE_NONE && (!(a->factor >= 1.0) || !isfinite(a->factor))) return BASISKV_ERR_INVALID_ARG;
+  if (kind >= BASISKV_ROPE_YARN && !positive(a->original_len)) return BASISKV_ERR_INVALID_ARG;
+  if (kind == BASISKV_ROPE_YARN && (!positive(a->beta_slow) || !positive(a->beta_fast) || a->beta_fast <= a->beta_slow))
+    return BASISKV_ERR_INVALID_ARG;
+  if (kind == BASISKV_ROPE_LLAMA3 && (!positive(a->low_freq_factor) || !positive(a->high_freq_factor) ||
+                                      a->high_freq_factor <= a->low_freq_factor))
+    return BASISKV_ERR_INVALID_ARG;
+  const double two_pi = 6.283185307179586477;
+  double base = a->base;
+  if (kind == BASISKV_ROPE_NTK && D > 2) base *= pow(a->factor, (double)D / (D - 2));
+  double lo = 0.0, hi = 0.0;  // yarn: the ramp's pairs
+  if (kind == BASISKV_ROPE_YARN) {
+    auto pair_of = [&](double turns) { return D * log(a->original_len / (turns * two_pi)) / (2.0 * log(base)); };
+    lo = fmax(floor(pair_of(a->beta_fast)), 0.0);
+    hi = fmin(ceil(pair_of(a->beta_slow)), (double)(D - 1));
+  }
+  *rope = basiskv_rope{};
+  rope->layout = a->layout;
+  rope->rotary_dim = D;
+  rope->mscale = (kind == BASISKV_ROPE_YARN && a->factor > 1.0) ? (float)(0.1 * log(a->factor) + 1.0) : 1.0f;
+  for (int i = 0; i < D / 2; ++i) {
+    double f = pow(base, -2.0 * i / D);
+    if (kind == BASISKV_ROPE_LINEAR) {
+      f /= a->factor;
+    } else if (kind == BASISKV_ROPE_YARN) {
+      const double ramp = fmin(fmax((i - lo) / fmax(hi - lo, 0.001), 0.0), 1.0);
+      f = f / a->factor * ramp + f * (1.0 - ramp);
+    } else if (kind == BASISKV_ROPE_LLAMA3) {
+      const double turns = a->original_len * f / two_pi;
+      const double mix = fmin(fmax((turns - a->low_freq_factor) / (a->high_freq_factor - a->low_freq_factor), 0.0), 1.0);
+      f = (1.0 - mix) * f / a->factor + mix * f;
+    }
+    rope->inv_freq[i] = f;
+  }
+  return BASISKV_OK;
+}
+
+basiskv_status basiskv_rotary(const basiskv_config* cfg, const basiskv_rope* rope, const void* q, int64_t q_stride,
+                              const void* k, int64_t k_stride, void* q_out, void* k_out, const int32_t* positions,
+                              const int32_t* seq_len, int32_t batch, int32_t n_new, void* stream) {
+  basiskv_status s = check_config(cfg);
+  if (s != BASISKV_OK) return s;
+  if (!rope || batch < 0 || n_new < 0) return BASISKV_ERR_INVALID_ARG;
+  if ((rope->layout != BASISKV_ROPE_HALF && rope->layout != BASISKV_ROPE_INTERLEAVED) || rope->rotary_dim < 2 ||
+      rope->rotary_dim % 2 != 0 || rope->rotary_dim > cfg->head_dim)
+    return BASISKV_ERR_INVALID_ARG;
+  if (batch == 0 || n_new == 0) return BASISKV_OK;
+  if ((!q && !k) || (!q) != (!q_out) || (!k) != (!k_out) || (!positions) == (!seq_len)) return BASISKV_ERR_INVALID_ARG;
+  const int64_t qd = (int64_t)cfg->num_q_heads * cfg->head_dim, kd = (int64_t)cfg->num_kv_heads * cfg->head_dim;
+  if ((q && q_stride < qd) || (k && k_stride < kd)) return BASISKV_ERR_INVALID_ARG;
+  if ((q && q == q_out && q_stride != qd) || (k && k == k_out && k_stride != kd)) return BASISKV_ERR_INVALID_ARG;
+  const uintptr_t es = esize(cfg);
+  for (const void* x : {q, k, (const void*)q_out, (const void*)k_out})
+    if (reinterpret_cast<uintptr_t>(x) % es != 0) return BASISKV_ERR_INVALID_ARG;
+  RotaryParams p{q, k, q_out, k_out, positions, seq_len, q ? q_stride : 0, k ? k_stride : 0, (long long)batch * n_new,
+                 n_new, q ? cfg->num_q_heads : 0, k ? cfg->num_kv_heads : 0, cfg->head_dim, rope->rotary_dim, 0, *rope};
+  return cuda_status(launch_rotary(p, cfg->dtype == BASISKV_BF16, num_sms(), (cudaStream_t)stream));
+}
+
+static DensePlan plan_dense(const basiskv_config* c, int32_t batch, int32_t n_new, int32_t max_pages) {
+  return dense_plan(batch, n_new, c->num_q_heads, c->num_kv_heads, c->head_dim, c->rank_v, c->page_size, max_pages,
+                    c->dtype == BASISKV_BF16, num_sms());
+}
+
+size_t basiskv_dense_attn_workspace_bytes(const basiskv_config* cfg, int32_t batch, int32_t n_new, int32_t max_pages) {
+  if (check_config(cfg) != BASISKV_OK || batch <= 0 || n_new <= 0 || max_pages <= 0 || max_pages > kMaxPagesLimit ||
+      batch > kMaxBatch || (long long)n_new > (long long)max_pages * cfg->page_size)
+    return 0;
+  return plan_dense(cfg, batch, n_new, max_pages).bytes;
+}
+
+basiskv_status basiskv_dense_attn(const basiskv_config* cfg, const basiskv_cache* cache, const void* q, int32_t batch,
+                                  int32_t n_new, const basiskv_attn_options* options, float* o_lat, float* lse,
+                                  void* ws, size_t ws_bytes, int32_t* err_flag, void* stream) {
+  basiskv_status s = check_config(cfg);
+  if (s != BASISKV_OK) return s;
+  if (batch < 0 || n_new < 0) return BASISKV_ERR_INVALID_ARG;
+  if (batch > kMaxBatch) return BASISKV_ERR_UNSUPPORTED;
+  const basiskv_attn_options o = options ? *options : basiskv_attn_options{};
+  if (!(o.scale >= 0.f) || !isfinite(o.scale) || !(o.softcap >= 0.f) || !isfinite(o.softcap) || o.window < 0)
+    return BASISKV_ERR_INVALID_ARG;
+  if (batch == 0 || n_new == 0) return BASISKV_OK;
+  if ((s = check_cache(cfg, cache, false, false)) != BASISKV_OK) return s;
+  if (!q || !o_lat || !err_flag || !aligned16(q) || !aligned16(o_lat)) return BASISKV_ERR_INVALID_ARG;
+  if ((long long)n_new > (long long)cache->max_pages * cfg->page_size) return BASISKV_ERR_INVALID_ARG;
+  const DensePlan pl = plan_dense(cfg, batch, n_new, cache->max_pages);
+  if (!ws || ws_bytes < pl.bytes || !aligned16(ws)) return BASISKV_ERR_WORKSPACE;
+  const bool swz_on = kc_swizzled(cfg->dtype == BASISKV_BF16, cfg->head_dim, cfg->rank_v);
+  const double scale = o.scale > 0.f ? (double)o.scale : 1.0 / sqrt((double)cfg->head_dim);
+  DenseParams p{};
+  p.q = q;
+  p.k_raw = cache->k_raw;
+  p.c_lat = cache->c_lat;
+  p.block_table = cache->block_table;
+  p.seq_len = cache->seq_len;
+  p.slopes = o.slopes;
+  p.prefix_len = o.prefix_len;
+  p.o = o_lat;
+  p.lse = lse;
+  p.err = err_flag;
+  p.batch = batch;
+  p.n_new = n_new;
+  p.Hq = cfg->num_q_heads;
+  p.Hkv = cfg->num_kv_heads;
+  p.G = cfg->num_q_heads / cfg->num_kv_heads;
+  p.d = cfg->head_dim;
+  p.r = cfg->rank_v;
+  p.page = cfg->page_size;
+  p.max_pages = cache->max_pages;
+  p.num_phys = cache->num_phys_pages;
+  p.window = o.window;
+  p.mk = swz_on ? swz_mask(cfg->head_dim) : 0;
+  p.mc = swz_on ? swz_mask(cfg->rank_v) : 0;
+  p.scale = (float)(o.softcap > 0.f ? scale / o.softcap : scale * 1.4426950408889634);
+  p.cap = (float)((double)o.softcap * 1.4426950408889634);
+  return cuda_status(launch_dense_attn(pl, p, cfg->dtype == BASISKV_BF16, ws, (cudaStream_t)stream));
 }
 
 basiskv_status basiskv_fuse_out_factor(const basiskv_config* cfg, const void* Bf, const void* W_O,

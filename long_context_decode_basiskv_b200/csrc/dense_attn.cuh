@@ -1,0 +1,157 @@
+// What the kernels of basiskv_dense_attn share: the parameter block, which keys
+// a row sees, what becomes of a raw score, and the joining of a split axis.
+//
+// A row is one (new token t, query head h) of a sequence; its position is
+// i = L - n_new + t.  Its score for key j and what it does with it:
+//   s = scale q.k_j;  s = cap tanh(s / cap) (cap > 0);  s -= slope_h |i - j|
+//   sees j:  j < L and ((j <= i and (window = 0 or i - j < window)) or j < prefix)
+//   o = sum_j softmax(s)_j C_j,  lse = log sum_j exp(s_j)
+// Scores are kept in units of log 2, so that a weight is one exp2.
+#pragma once
+
+#include "common.cuh"
+
+namespace bkv {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct DenseParams {
+  const void* q;               // [B][n_new][Hq][d]
+  const void* k_raw;
+  const void* c_lat;
+  const int32_t* block_table;
+  const int32_t* seq_len;
+  const float* slopes;         // [Hq] or NULL
+  const int32_t* prefix_len;   // [B] or NULL
+  float* o;                    // [B][n_new][Hq][r]
+  float* lse;                  // [B][n_new][Hq] or NULL
+  int32_t* err;
+  float* part;                 // partial results of splits: per row (max, sum, acc[r])
+  int32_t* cnt;                // finished splits of each unit, zero between calls
+  int batch, n_new, Hq, Hkv, G, d, r, page, max_pages, num_phys;
+  int window;
+  int mk, mc;                  // row swizzle of K and C pages (swz())
+  int splits;
+  float scale;                 // plain scores: scale log2(e); capped: scale / cap
+  float cap;                   // 0, or cap log2(e)
+};
+
+// Raw score -> score in units of log 2.  MOD = false: neither cap nor slopes
+// (the scale is then folded into the exponent by the caller).
+// tanh(x) = 1 - 2 / (1 + e^2x): with the fast exponential and reciprocal its
+// absolute error is about 2e-7, that is 2e-7 cap in a score (cap 50: 1e-5 of a
+// weight); small arguments, where 1 - 2 / (1 + e^2x) would cancel, take the
+// Taylor series to x^7 (|x| < 0.15: its remainder is below 1e-9).
+__device__ __forceinline__ float cap_score(float x, float cap) {  // x = s / cap
+  const float x2 = x * x;
+  const float series = x * fmaf(x2, fmaf(x2, fmaf(x2, -17.f / 315.f, 2.f / 15.f), -1.f / 3.f), 1.f);
+  const float e = exp2f(x * (2.f * kLog2e));
+  const float far = 1.f - __fdividef(2.f, 1.f + e);
+  return cap * (x2 < 0.0225f ? series : far);
+}
+
+__device__ __forceinline__ float mod_score(float raw, float scale, float cap, float slope2, int i, int j) {
+  float s = raw * scale;
+  if (cap > 0.f) s = cap_score(s, cap);
+  return s - slope2 * fabsf((float)(i - j));
+}
+
+__device__ __forceinline__ bool sees(int i, int j, int L, int window, int prefix) {
+  return j < L && ((j <= i && (window == 0 || i - j < window)) || j < prefix);
+}
+
+// Keys that rows at positions [i0, i1] of a sequence see, as tiles of `tile`
+// keys: tiles [0, na) and [nb, ne), na <= nb.
+struct KeyTiles {
+  int na, nb, ne;
+  __device__ __forceinline__ int count() const { return na + ne - nb; }
+  __device__ __forceinline__ int tile(int x) const { return x < na ? x : x - na + nb; }
+};
+__device__ __forceinline__ KeyTiles key_tiles(int i0, int i1, int L, int window, int prefix, int tile) {
+  KeyTiles k;
+  const int end = min(L, max(i1 + 1, prefix));
+  k.ne = (end + tile - 1) / tile;
+  const int lo = window > 0 ? max(0, i0 - window + 1) : 0;
+  k.na = min(k.ne, (min(prefix, end) + tile - 1) / tile);
+  k.nb = min(k.ne, max(k.na, lo / tile));
+  return k;
+}
+
+// A sequence as the kernels take it: its length (0: nothing to attend over),
+// its prefix clamped to the length.
+struct DenseSeq {
+  int L, prefix;
+};
+__device__ __forceinline__ DenseSeq dense_seq(const DenseParams& p, int b, bool report) {
+  DenseSeq s{p.seq_len[b], 0};
+  if (s.L < 0 || (s.L > 0 && s.L < p.n_new) || s.L > p.max_pages * p.page) {
+    if (report) set_err(p.err, BASISKV_DEVERR_SEQ_LEN);
+    s.L = 0;
+  }
+  if (p.prefix_len) s.prefix = max(0, min(s.L, p.prefix_len[b]));
+  return s;
+}
+
+// physical page of a logical page, -1 (reported) where the table's entry is out of range
+__device__ __forceinline__ int dense_page(const DenseParams& p, int b, int page) {
+  const int id = p.block_table[(size_t)b * p.max_pages + page];
+  if (id < 0 || id >= p.num_phys) {
+    set_err(p.err, BASISKV_DEVERR_BLOCK_TABLE);
+    return -1;
+  }
+  return id;
+}
+
+// Counts this CTA among the splits of its unit; true in every thread of the
+// last one, which joins their results.  The counter is left at zero.
+__device__ __forceinline__ bool dense_last_split(int32_t* cnt, int splits, int32_t* err, int* s_last) {
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    const int prev = atomicAdd(cnt, 1);
+    if (prev >= splits) set_err(err, BASISKV_DEVERR_WORKSPACE);
+    *s_last = prev == splits - 1;
+    if (*s_last) {
+      *cnt = 0;
+      __threadfence();
+    }
+  }
+  __syncthreads();
+  return *s_last != 0;
+}
+
+// One warp joins a row's partial results, `stride` floats apart, and writes
+// the row: o = sum_s 2^(m_s - M) acc_s / sum_s 2^(m_s - M) l_s.
+__device__ __forceinline__ void dense_join_row(const float* part, size_t stride, int splits, int r, float* o,
+                                               float* lse, int lane) {
+  float M = -INFINITY;
+  for (int s = lane; s < splits; s += 32) M = fmaxf(M, __ldcg(part + s * stride));
+  M = warp_max(M);
+  float l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+  if (M != -INFINITY) {
+    for (int s0 = 0; s0 < splits; s0 += 32) {
+      float w = 0.f;
+      if (s0 + lane < splits) {
+        w = exp2f(__ldcg(part + (s0 + lane) * stride) - M);
+        l += w * __ldcg(part + (s0 + lane) * stride + 1);
+      }
+      const int n = min(32, splits - s0);
+      for (int s = 0; s < n; ++s) {
+        const float ws = __shfl_sync(kFull, w, s);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (lane + 32 * k < r) acc[k] = fmaf(ws, __ldcg(part + (s0 + s) * stride + 2 + lane + 32 * k), acc[k]);
+      }
+    }
+  }
+  if (M == -INFINITY)  // nothing was seen, or nothing but NaN: sums of 0 or NaN
+    for (int s = lane; s < splits; s += 32) l += __ldcg(part + s * stride + 1);
+  l = warp_sum(l);
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (lane + 32 * k < r) o[lane + 32 * k] = l > 0.f ? acc[k] / l : (l == l ? 0.f : l);
+  if (lse && lane == 0) *lse = l > 0.f ? (M + log2f(l)) * kLn2 : (l == l ? -INFINITY : l);
+}
+
+}  // namespace bkv

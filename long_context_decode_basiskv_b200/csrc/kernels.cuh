@@ -140,6 +140,47 @@ cudaError_t launch_out_proj_tc(const float* o, const void* Gt, float* y, int32_t
 // bytes from src to dst by the SMs (either side device memory or mapped host memory)
 cudaError_t launch_copy(void* dst, const void* src, size_t bytes, int num_sms, cudaStream_t st);
 
+// Page assignment (amount: new tokens of each request) and release (amount: nonzero for requests that end).
+struct PagesParams {
+  const int32_t* seq_len;
+  const int32_t* amount;
+  int32_t* table;
+  int32_t* free_pages;
+  const int32_t* free_count;
+  int32_t* seq_len_out;
+  int32_t* free_count_out;
+  int32_t* slots;  // [B][slot_cols] or NULL
+  int32_t* err;
+  int batch, page, max_pages, num_phys, slot_cols, slot_vec;
+};
+cudaError_t launch_assign_pages(const PagesParams& p, cudaStream_t st);
+cudaError_t launch_release_pages(const PagesParams& p, cudaStream_t st);
+
+struct RotaryParams {
+  const void* q;
+  const void* k;
+  void* q_out;
+  void* k_out;
+  const int32_t* positions;  // [tokens], or NULL: from seq_len
+  const int32_t* seq_len;
+  long long q_stride, k_stride;  // elements from one token to the next
+  long long tokens;
+  int n_new, hq, hk, d, rot, tokens_per_cta;
+  basiskv_rope rope;
+};
+cudaError_t launch_rotary(RotaryParams p, bool bf16, int num_sms, cudaStream_t st);
+
+// Attention over the whole cache: grid and scratch of one call, from the shape only.
+struct DensePlan {
+  int row_tile;  // rows (new token, head) of a tile
+  int splits;    // shares of the keys
+  size_t cnt_off, part_off, bytes;
+};
+struct DenseParams;
+DensePlan dense_plan(int batch, int n_new, int Hq, int Hkv, int d, int r, int page, int max_pages, bool bf16,
+                     int num_sms);
+cudaError_t launch_dense_attn(const DensePlan& pl, DenseParams p, bool bf16, void* scratch, cudaStream_t st);
+
 struct FuseParams {
   const void* Bf;
   const void* W_O;

@@ -1,0 +1,191 @@
+// Pages of the cache for requests that grow or end: block-table entries and
+// token slots from the requests' lengths, on the device.
+//
+//   have_b = ceil(L_b / P),  need_b = ceil((L_b + a_b) / P) - have_b,  off_b = sum_{c < b} need_c
+//   new page i of all (request b, i = off_b + x)  ->  free[count - 1 - i]  at  table[b][have_b + x]
+//   token t of request b                          ->  slot = page * P + (L_b + t) % P
+//
+// and the reverse for requests that end.  The work is a few integers per page
+// or token, so the call is latency: one launch, one thread-block cluster.
+// Every CTA of the cluster scans the lengths by itself (they come from L2) and
+// keeps lengths and offsets in shared memory; a cluster barrier stands between
+// the last read of seq_len / free_count and the first write, so the outputs
+// may be the inputs (a captured graph steps in place), and carries each CTA's
+// fault bits to the others, so a call that cannot be met in full changes
+// nothing.
+#include "kernels.cuh"
+
+namespace bkv {
+
+constexpr int kPageThreads = 1024;
+// A cluster of 8 CTAs (the portable limit) for anything but the smallest
+// calls, whose few stores one CTA issues as fast without the cluster's start.
+constexpr int kPageCluster = 8;
+constexpr long long kPageSmall = 8192;  // slots, or requests, that one CTA serves
+
+// the request that page p of the flattened new (or released) pages belongs to
+__device__ __forceinline__ int request_of(const int* off, int B, int p) {
+  int lo = 0, hi = B;  // off[lo] <= p < off[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (off[mid] <= p) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+template <bool ASSIGN>
+__global__ void __launch_bounds__(kPageThreads) pages_kernel(PagesParams p) {
+  extern __shared__ int s_len[];        // [B] lengths, then [B + 1] offsets
+  __shared__ int warp_tot[32];
+  __shared__ uint32_t s_bad;
+  const int tid = threadIdx.x, B = p.batch, P = p.page, sh = 31 - __clz(P);
+  const int C = gridDim.x, rank = blockIdx.x;  // one cluster: its rank is the block index
+  int* s_off = s_len + B;
+  if (tid == 0) s_bad = 0;
+  __syncthreads();
+
+  // pages of each request, their exclusive sums
+  const int per = (B + kPageThreads - 1) / kPageThreads;
+  const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
+  uint32_t bad = 0;
+  int sum = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int L = p.seq_len[b], a = p.amount[b];
+    const long long end = ASSIGN ? (long long)L + a : L;
+    int n = 0;
+    if (L < 0 || (ASSIGN && a < 0) || end > (long long)p.max_pages * P)
+      bad |= BASISKV_DEVERR_SEQ_LEN;
+    else if (ASSIGN)
+      n = (int)((end + P - 1) >> sh) - ((L + P - 1) >> sh);
+    else if (a != 0)
+      n = (L + P - 1) >> sh;
+    s_len[b] = L;
+    s_off[b] = n;
+    sum += n;
+  }
+  int total;
+  int at = block_exclusive_scan(sum, warp_tot, total);
+  for (int b = b0; b < b1; ++b) {
+    const int n = s_off[b];
+    s_off[b] = at;
+    at += n;
+  }
+  if (tid == 0) s_off[B] = total;
+  const int count = *p.free_count;
+  if (count < 0 || count > p.num_phys || (ASSIGN ? total > count : total > p.num_phys - count))
+    bad |= BASISKV_DEVERR_PAGES;
+  __syncthreads();
+
+  // the page ids this call hands on, checked before anything is written
+  const int gt = rank * kPageThreads + tid, nt = C * kPageThreads;
+  if (!(bad & BASISKV_DEVERR_PAGES)) {  // the same for every thread of the cluster
+    for (int i = gt; i < total; i += nt) {
+      int id;
+      if (ASSIGN) {
+        id = p.free_pages[count - 1 - i];
+      } else {
+        const int b = request_of(s_off, B, i);
+        id = p.table[(size_t)b * p.max_pages + (i - s_off[b])];
+      }
+      if (id < 0 || id >= p.num_phys) bad |= BASISKV_DEVERR_BLOCK_TABLE;
+    }
+  }
+  if (ASSIGN && p.slots) {  // a partly filled page that takes the first new tokens
+    for (int b = gt; b < B; b += nt) {
+      const int L = s_len[b];
+      if (L <= 0 || (L & (P - 1)) == 0 || L > p.max_pages * P || p.amount[b] <= 0) continue;
+      const int id = p.table[(size_t)b * p.max_pages + (L >> sh)];
+      if (id < 0 || id >= p.num_phys) bad |= BASISKV_DEVERR_BLOCK_TABLE;
+    }
+  }
+  if (bad) atomicOr(&s_bad, bad);
+  __syncthreads();
+  bad = s_bad;
+  if (C > 1) {  // the others' bits; nobody leaves while its own may still be read
+    cluster_arrive_release();
+    cluster_wait_acquire();
+    for (int c = 0; c < C; ++c) bad |= ld_shared_cluster(&s_bad, (uint32_t)c);
+    cluster_arrive_relaxed();
+  }
+
+  if (rank == 0) {
+    for (int b = tid; b < B; b += kPageThreads) {
+      const int L = s_len[b];
+      p.seq_len_out[b] = bad ? L : ASSIGN ? L + p.amount[b] : p.amount[b] != 0 ? 0 : L;
+    }
+    if (tid == 0) {
+      *p.free_count_out = bad ? count : ASSIGN ? count - total : count + total;
+      if (bad) set_err(p.err, (int32_t)bad);
+    }
+  }
+  if (!bad) {
+    for (int i = gt; i < total; i += nt) {
+      const int b = request_of(s_off, B, i);
+      if (ASSIGN)
+        p.table[(size_t)b * p.max_pages + ((s_len[b] + P - 1) >> sh) + (i - s_off[b])] = p.free_pages[count - 1 - i];
+      else
+        p.free_pages[count + i] = p.table[(size_t)b * p.max_pages + (i - s_off[b])];
+    }
+  }
+  if (ASSIGN && p.slots) {
+    const int v = p.slot_vec, cols = p.slot_cols / v;  // v slots to a store
+    const int db = nt / cols, dc = nt - db * cols;
+    int b = gt / cols, c = gt - b * cols;
+    while (b < B) {
+      int w[4] = {-1, -1, -1, -1};
+      const int t0 = c * v, a = bad ? 0 : p.amount[b];
+      if (t0 < a) {
+        const int L = s_len[b], have = (L + P - 1) >> sh;
+        int page = -1, id = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (j < v && t0 + j < a) {
+            const int pos = L + t0 + j, pg = pos >> sh;
+            if (pg != page) {
+              page = pg;
+              id = pg < have ? p.table[(size_t)b * p.max_pages + pg] : p.free_pages[count - 1 - (s_off[b] + pg - have)];
+            }
+            w[j] = (id << sh) + (pos & (P - 1));
+          }
+        }
+      }
+      int* out = p.slots + (size_t)b * p.slot_cols + t0;
+      if (v == 4) *reinterpret_cast<int4*>(out) = make_int4(w[0], w[1], w[2], w[3]);
+      else *out = w[0];
+      b += db;
+      c += dc;
+      if (c >= cols) {
+        c -= cols;
+        ++b;
+      }
+    }
+  }
+  if (C > 1) cluster_wait_acquire();
+}
+
+template <bool ASSIGN>
+static cudaError_t launch_pages_t(const PagesParams& p, cudaStream_t st) {
+  const size_t smem = ((size_t)2 * p.batch + 1) * sizeof(int);
+  cudaError_t e = ensure_smem((const void*)pages_kernel<ASSIGN>, smem);
+  if (e != cudaSuccess) return e;
+  const long long slots = (ASSIGN && p.slots) ? (long long)p.batch * p.slot_cols : (long long)p.batch * 128;
+  const int C = slots <= kPageSmall ? 1 : kPageCluster;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(C);
+  cfg.blockDim = dim3(kPageThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, pages_kernel<ASSIGN>, p);
+}
+
+cudaError_t launch_assign_pages(const PagesParams& p, cudaStream_t st) { return launch_pages_t<true>(p, st); }
+cudaError_t launch_release_pages(const PagesParams& p, cudaStream_t st) { return launch_pages_t<false>(p, st); }
+
+}  // namespace bkv

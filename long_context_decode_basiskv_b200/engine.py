@@ -13,12 +13,18 @@ the tensor-core path for long appends).  ``overlap`` picks how append and
 route overlap: "pdl" (one call, basiskv_append_route: the scoring runs
 beside the append as its programmatic dependent, one stream) or "streams"
 (basiskv_append on a forked stream beside basiskv_route, then a join).
+``attention`` "dense" attends over the whole cache instead of the routed pages
+(append, dense_attn with ``options``, out_proj).  ``rope`` rotates the step's
+queries and keys, and the prefilled keys, by their positions before they are
+used.  ``paging`` "pool" takes the block table from a PagePool on the device
+instead of from the case.
 """
 from __future__ import annotations
 
 import torch
 
 from . import binding as bk
+from .pages import PagePool
 from .workloads import Case
 
 
@@ -33,12 +39,20 @@ _GROUP_REDUCE = {"group_sum": bk.GROUP_SUM, "group_max": bk.GROUP_MAX}
 
 class DecodeEngine:
     def __init__(self, case: Case, device="cuda", stream=None, routing: str = "head",
-                 prefill_mode: str = "exact", overlap: str = "pdl"):
+                 prefill_mode: str = "exact", overlap: str = "pdl", attention: str = "routed",
+                 options: bk.AttnOptions = None, rope: bk.Rope = None, paging: str = "case"):
         if routing != "head" and routing not in _GROUP_REDUCE:
             raise ValueError(f"routing must be 'head', 'group_sum' or 'group_max', not {routing!r}")
         if overlap not in ("pdl", "streams"):
             raise ValueError(f"overlap must be 'pdl' or 'streams', not {overlap!r}")
         self.overlap = overlap
+        if attention not in ("routed", "dense"):
+            raise ValueError(f"attention must be 'routed' or 'dense', not {attention!r}")
+        if options is not None and attention != "dense":
+            raise ValueError("options are the dense attention's")
+        if paging not in ("case", "pool"):
+            raise ValueError(f"paging must be 'case' or 'pool', not {paging!r}")
+        self.attention, self.options, self.rope = attention, options, rope
         if prefill_mode not in ("exact", "tc"):
             raise ValueError(f"prefill_mode must be 'exact' or 'tc', not {prefill_mode!r}")
         self.routing = routing
@@ -49,14 +63,19 @@ class DecodeEngine:
         dev = self.device
         B = case.wl.batch
         lengths = torch.tensor(case.lengths, dtype=torch.int32)
-        self.cache = bk.PagedCache(cfg, case.num_phys_pages, case.block_table, lengths, device=dev)
+        self.err = torch.zeros(1, dtype=torch.int32, device=dev)
+        table = case.block_table
+        if paging == "pool":
+            self.pool = PagePool(cfg, case.num_phys_pages, B, case.max_pages, device=dev)
+            self.pool.extend(lengths.to(dev), self.err, stream=stream)
+            table, lengths = self.pool.block_table, self.pool.seq_len
+        self.cache = bk.PagedCache(cfg, case.num_phys_pages, table, lengths, device=dev)
         self.factors = bk.Factors(case.A.to(dev).contiguous(), case.P.to(dev).contiguous(),
                                   case.E.to(dev).contiguous(),
                                   torch.empty((cfg.hidden, cfg.num_q_heads, cfg.rank_v),
                                               dtype=cfg.dtype, device=dev))
         bk.fuse_out_factor(cfg, case.Bf.to(dev).contiguous(), case.W_O.to(dev).contiguous(),
                            self.factors.Gt, stream)
-        self.err = torch.zeros(1, dtype=torch.int32, device=dev)
         self.ws = bk.alloc_workspace(cfg, B, self.cache.max_pages, device=dev)
         # step inputs: the last token of every sequence, and the query; q, k_new
         # and v_new are views of one device buffer, so a caller can refresh all
@@ -74,6 +93,12 @@ class DecodeEngine:
             views.append(v)
             off += n
         self.q, self.k_new, self.v_new = views
+        # what the step appends and attends with: the inputs, or the rotated inputs
+        self.q_in, self.k_in = self.q, self.k_new
+        if rope is not None:
+            self.q, self.k_new = torch.empty_like(self.q_in), torch.empty_like(self.k_in)
+        if attention == "dense":
+            self.dense_ws = bk.alloc_dense_workspace(cfg, B, 1, self.cache.max_pages, device=dev)
         # step outputs
         self.sel = torch.empty((B, cfg.num_q_heads, cfg.top_k + 2), dtype=torch.int32, device=dev)
         self.sel_cnt = torch.empty((B, cfg.num_q_heads), dtype=torch.int32, device=dev)
@@ -98,8 +123,17 @@ class DecodeEngine:
             sub.seq_len = torch.tensor([L - 1], dtype=torch.int32, device=dev)
             k = case.keys[b][:-1].to(dev).unsqueeze(0).contiguous()
             v = case.values[b][:-1].to(dev).unsqueeze(0).contiguous()
+            if self.rope is not None:
+                plain, k = k, torch.empty_like(k)  # the case keeps its keys
+                bk.rotary(cfg, self.rope, None, plain, None, k, seq_len=sub.seq_len, stream=stream)
             fn = bk.prefill if self.prefill_mode == "tc" else bk.append
             fn(cfg, sub, self.factors, k, v, self.err, stream)
+
+    def rotary(self, stream=None):
+        """The step's queries and keys, rotated to the new token's position (nothing without rope)."""
+        if self.rope is not None:
+            bk.rotary(self.cfg, self.rope, self.q_in.unsqueeze(1), self.k_in, self.q.unsqueeze(1), self.k_new,
+                      seq_len=self.cache.seq_len, stream=stream)
 
     def append(self, stream=None):
         bk.append(self.cfg, self.cache, self.factors, self.k_new, self.v_new, self.err, stream)
@@ -116,6 +150,10 @@ class DecodeEngine:
         the workspace; from_route=False passes sel / sel_cnt (the library rebuilds them)."""
         sel, cnt = (None, None) if from_route else (self.sel, self.sel_cnt)
         bk.decode_attn(self.cfg, self.cache, self.q, sel, cnt, self.o_lat, self.ws, self.err, stream)
+
+    def dense_attn(self, stream=None, lse=None):
+        """Attention of the step's token over the whole cache, with the engine's options."""
+        bk.dense_attn(self.cfg, self.cache, self.q, self.o_lat, self.dense_ws, self.err, self.options, lse, stream)
 
     def out_proj(self, stream=None, y=None):
         """y defaults to the engine's device tensor; a pinned CPU tensor of its shape
@@ -141,6 +179,11 @@ class DecodeEngine:
             self._fork = torch.cuda.Event()
             self._join = torch.cuda.Event()
         nq = self.q.numel()
+        if self.rope is not None:  # the rotation comes before both, so there is nothing to fork
+            if host_in is not None:
+                bk.copy(self._inbuf, host_in, main)
+                host_in = None
+            self.rotary(main)
         if self.overlap == "pdl":
             if host_in is not None:
                 bk.copy(self._inbuf, host_in, main)
@@ -162,7 +205,15 @@ class DecodeEngine:
     def step(self, stream=None, y=None, host_in=None):
         """One decode step: (append || route) -> decode_attn -> out_proj (into y, by
         default the engine's device tensor; inputs from `host_in` when given, see
-        append_route)."""
+        append_route).  With dense attention: rotary, append -> dense_attn -> out_proj."""
+        if self.attention == "dense":
+            if host_in is not None:
+                bk.copy(self._inbuf, host_in, stream)
+            self.rotary(stream)
+            self.append(stream)
+            self.dense_attn(stream)
+            self.out_proj(stream, y)
+            return self.y if y is None else y
         self.append_route(stream, host_in)
         self.decode_attn(stream)
         self.out_proj(stream, y)
