@@ -159,7 +159,8 @@ __global__ void __launch_bounds__(kDcThreads) dense_attn_kernel(DenseParams p) {
   for (int rr = warp; rr < rows; rr += 4) {
     const int row = row0 + rr;
     const size_t at = ((size_t)b * p.n_new + row / p.G) * p.Hq + (size_t)g * p.G + row % p.G;
-    dense_join_row(part + (size_t)rr * (r + 2), stride, p.splits, r, p.o + at * r, p.lse ? p.lse + at : nullptr, lane);
+    dense_join_row(part + (size_t)rr * (r + 2), stride, p.splits, r, p.o + at * r, p.lse ? p.lse + at : nullptr, lane,
+                   false);
   }
 }
 
@@ -170,10 +171,13 @@ static int core_rows(int rows) { return rows <= 8 ? 8 : 32; }
 // cache that fills its block table.
 DensePlan dense_plan(int batch, int n_new, int Hq, int Hkv, int d, int r, int page, int max_pages, bool bf16,
                      int num_sms) {
-  (void)d;
-  (void)bf16;
   DensePlan pl{};
   const long long rows = (long long)n_new * (Hq / Hkv);
+  if (kc_swizzled(bf16, d, r) && rows <= 16) {
+    pl.row_tile = 0;
+    dense_plan_mma(&pl, batch, (int)rows, Hkv, d, r, page, max_pages, num_sms);
+    return pl;
+  }
   pl.row_tile = core_rows((int)std::min(rows, 1000LL));
   const long long tiles = (rows + pl.row_tile - 1) / pl.row_tile;
   const long long units = tiles * Hkv * batch;
@@ -208,6 +212,7 @@ cudaError_t launch_dense_attn(const DensePlan& pl, DenseParams p, bool bf16, voi
   p.cnt = reinterpret_cast<int32_t*>(base + pl.cnt_off);
   p.part = reinterpret_cast<float*>(base + pl.part_off);
   p.splits = pl.splits;
+  if (pl.row_tile == 0) return launch_dense_mma(p, st);
   if (bf16)
     return p.d == 128 ? launch_core<__nv_bfloat16, 128>(p, pl.row_tile, st)
                       : launch_core<__nv_bfloat16, 64>(p, pl.row_tile, st);

@@ -121,37 +121,69 @@ __device__ __forceinline__ bool dense_last_split(int32_t* cnt, int splits, int32
   return *s_last != 0;
 }
 
-// One warp joins a row's partial results, `stride` floats apart, and writes
-// the row: o = sum_s 2^(m_s - M) acc_s / sum_s 2^(m_s - M) l_s.
-__device__ __forceinline__ void dense_join_row(const float* part, size_t stride, int splits, int r, float* o,
-                                               float* lse, int lane) {
-  float M = -INFINITY;
-  for (int s = lane; s < splits; s += 32) M = fmaxf(M, __ldcg(part + s * stride));
-  M = warp_max(M);
-  float l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-  if (M != -INFINITY) {
-    for (int s0 = 0; s0 < splits; s0 += 32) {
-      float w = 0.f;
-      if (s0 + lane < splits) {
-        w = exp2f(__ldcg(part + (s0 + lane) * stride) - M);
-        l += w * __ldcg(part + (s0 + lane) * stride + 1);
-      }
-      const int n = min(32, splits - s0);
-      for (int s = 0; s < n; ++s) {
-        const float ws = __shfl_sync(kFull, w, s);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (lane + 32 * k < r) acc[k] = fmaf(ws, __ldcg(part + (s0 + s) * stride + 2 + lane + 32 * k), acc[k]);
-      }
+// A warp's fold of a row's partial results, `stride` floats apart, in order:
+// M = max m_s, l = sum 2^(m_s - M) l_s (whole warp), acc likewise (columns
+// lane + 32 k).  Eight results' loads are in flight at a time.
+struct DenseFold {
+  float M, l, acc[4];
+};
+__device__ __forceinline__ DenseFold dense_fold(const float* part, size_t stride, int splits, int r, int lane) {
+  constexpr int kAt = 8;
+  DenseFold f{-INFINITY, 0.f, {0.f, 0.f, 0.f, 0.f}};
+  for (int s0 = 0; s0 < splits; s0 += kAt) {
+    const int n = min(kAt, splits - s0);
+    const float* at = part + s0 * stride;
+    float m = -INFINITY, l = 0.f, x[kAt][4];
+    if (lane < n) {
+      m = __ldcg(at + lane * stride);
+      l = __ldcg(at + lane * stride + 1);
     }
+#pragma unroll
+    for (int s = 0; s < kAt; ++s)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        x[s][k] = (s < n && lane + 32 * k < r) ? __ldcg(at + s * stride + 2 + lane + 32 * k) : 0.f;
+    const float M = fmaxf(f.M, warp_max(m));
+    // while nothing has been seen, sums are 0, or NaN where all scores were
+    const float c = M == -INFINITY ? 1.f : exp2f(f.M - M), w = M == -INFINITY ? 1.f : exp2f(m - M);
+    f.l = f.l * c + warp_sum(lane < n ? l * w : 0.f);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) f.acc[k] *= c;
+#pragma unroll
+    for (int s = 0; s < kAt; ++s) {
+      const float ws = __shfl_sync(kFull, w, s);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (s < n) f.acc[k] = fmaf(ws, x[s][k], f.acc[k]);
+    }
+    f.M = M;
   }
-  if (M == -INFINITY)  // nothing was seen, or nothing but NaN: sums of 0 or NaN
-    for (int s = lane; s < splits; s += 32) l += __ldcg(part + s * stride + 1);
-  l = warp_sum(l);
+  return f;
+}
+
+// The fold as one partial result.  failed: a wait gave up on the way; the sum
+// is NaN then, and with it every output that it goes into.
+__device__ __forceinline__ void dense_fold_row(const float* part, size_t stride, int splits, int r, float* to,
+                                               bool failed, int lane) {
+  const DenseFold f = dense_fold(part, stride, splits, r, lane);
+  if (lane == 0) {
+    to[0] = f.M;
+    to[1] = failed ? __int_as_float(0x7fc00000) : f.l;
+  }
 #pragma unroll
   for (int k = 0; k < 4; ++k)
-    if (lane + 32 * k < r) o[lane + 32 * k] = l > 0.f ? acc[k] / l : (l == l ? 0.f : l);
-  if (lse && lane == 0) *lse = l > 0.f ? (M + log2f(l)) * kLn2 : (l == l ? -INFINITY : l);
+    if (lane + 32 * k < r) to[2 + lane + 32 * k] = f.acc[k];
+}
+
+// The fold as the row's result.
+__device__ __forceinline__ void dense_join_row(const float* part, size_t stride, int splits, int r, float* o,
+                                               float* lse, int lane, bool failed) {
+  const DenseFold f = dense_fold(part, stride, splits, r, lane);
+  const float l = failed ? __int_as_float(0x7fc00000) : f.l;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (lane + 32 * k < r) o[lane + 32 * k] = l > 0.f ? f.acc[k] / l : (l == l ? 0.f : l);
+  if (lse && lane == 0) *lse = l > 0.f ? (f.M + log2f(l)) * kLn2 : (l == l ? -INFINITY : l);
 }
 
 }  // namespace bkv
