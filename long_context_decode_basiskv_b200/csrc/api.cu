@@ -451,7 +451,6 @@ basiskv_status basiskv_dense_attn(const basiskv_config* cfg, const basiskv_cache
   if ((long long)n_new > (long long)cache->max_pages * cfg->page_size) return BASISKV_ERR_INVALID_ARG;
   const DensePlan pl = plan_dense(cfg, batch, n_new, cache->max_pages);
   if (!ws || ws_bytes < pl.bytes || !aligned16(ws)) return BASISKV_ERR_WORKSPACE;
-  const bool swz_on = kc_swizzled(cfg->dtype == BASISKV_BF16, cfg->head_dim, cfg->rank_v);
   const double scale = o.scale > 0.f ? (double)o.scale : 1.0 / sqrt((double)cfg->head_dim);
   DenseParams p{};
   p.q = q;
@@ -475,8 +474,7 @@ basiskv_status basiskv_dense_attn(const basiskv_config* cfg, const basiskv_cache
   p.max_pages = cache->max_pages;
   p.num_phys = cache->num_phys_pages;
   p.window = o.window;
-  p.mk = swz_on ? swz_mask(cfg->head_dim) : 0;
-  p.mc = swz_on ? swz_mask(cfg->rank_v) : 0;
+  p.mc = swz_mask(cfg->rank_v);
   p.scale = (float)(o.softcap > 0.f ? scale / o.softcap : scale * 1.4426950408889634);
   p.cap = (float)((double)o.softcap * 1.4426950408889634);
   return cuda_status(launch_dense_attn(pl, p, cfg->dtype == BASISKV_BF16, ws, (cudaStream_t)stream));

@@ -79,11 +79,11 @@ __global__ void __launch_bounds__(kDcThreads) dense_attn_kernel(DenseParams p) {
     for (int y = tid; y < kDcKeys * D; y += kDcThreads) {
       const int jj = y / D, slot = (j0 + jj) % p.page;
       sK[jj * KP + y % D] = s_ok[jj] < 0 ? 0.f
-          : Elem<T>::to_f(kr[(((size_t)s_ok[jj] * p.Hkv + g) * p.page + slot) * D + swz(y % D, slot, p.mk)]);
+          : Elem<T>::to_f(kr[(((size_t)s_ok[jj] * p.Hkv + g) * p.page + slot) * D + y % D]);
     }
     for (int y = tid; y < kDcKeys * r; y += kDcThreads) {
       const int jj = y / r, slot = (j0 + jj) % p.page;
-      sC[y] = s_ok[jj] < 0 ? 0.f : Elem<T>::to_f(cl[(((size_t)s_ok[jj] * p.Hkv + g) * p.page + slot) * r + swz(y % r, slot, p.mc)]);
+      sC[y] = s_ok[jj] < 0 ? 0.f : Elem<T>::to_f(cl[(((size_t)s_ok[jj] * p.Hkv + g) * p.page + slot) * r + y % r]);
     }
     __syncthreads();
     float s[RW];
@@ -173,9 +173,10 @@ DensePlan dense_plan(int batch, int n_new, int Hq, int Hkv, int d, int r, int pa
                      int num_sms) {
   DensePlan pl{};
   const long long rows = (long long)n_new * (Hq / Hkv);
-  if (kc_swizzled(bf16, d, r) && rows <= 16) {
-    pl.row_tile = 0;
-    dense_plan_mma(&pl, batch, (int)rows, Hkv, d, r, page, max_pages, num_sms);
+  if (kc_swizzled(bf16, d, r)) {
+    pl.row_tile = rows <= 16 ? 0 : -1;
+    if (rows <= 16) dense_plan_mma(&pl, batch, (int)rows, Hkv, d, r, page, max_pages, num_sms);
+    else dense_plan_tc(&pl, batch, rows, Hkv, r, page, max_pages, num_sms);
     return pl;
   }
   pl.row_tile = core_rows((int)std::min(rows, 1000LL));
@@ -213,6 +214,7 @@ cudaError_t launch_dense_attn(const DensePlan& pl, DenseParams p, bool bf16, voi
   p.part = reinterpret_cast<float*>(base + pl.part_off);
   p.splits = pl.splits;
   if (pl.row_tile == 0) return launch_dense_mma(p, st);
+  if (pl.row_tile < 0) return launch_dense_tc(p, st);
   if (bf16)
     return p.d == 128 ? launch_core<__nv_bfloat16, 128>(p, pl.row_tile, st)
                       : launch_core<__nv_bfloat16, 64>(p, pl.row_tile, st);

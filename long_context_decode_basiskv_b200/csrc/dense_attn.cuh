@@ -31,11 +31,19 @@ struct DenseParams {
   int32_t* cnt;                // finished splits of each unit, zero between calls
   int batch, n_new, Hq, Hkv, G, d, r, page, max_pages, num_phys;
   int window;
-  int mk, mc;                  // row swizzle of K and C pages (swz())
+  int mc;                      // row swizzle of C pages (swz())
   int splits;
   float scale;                 // plain scores: scale log2(e); capped: scale / cap
   float cap;                   // 0, or cap log2(e)
 };
+
+// 2^x by the hardware's instruction (2 units in the last place; results below the normal range are 0,
+// which no sum of weights around 1 notices).
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 // Raw score -> score in units of log 2.  MOD = false: neither cap nor slopes
 // (the scale is then folded into the exponent by the caller).
@@ -46,7 +54,7 @@ struct DenseParams {
 __device__ __forceinline__ float cap_score(float x, float cap) {  // x = s / cap
   const float x2 = x * x;
   const float series = x * fmaf(x2, fmaf(x2, fmaf(x2, -17.f / 315.f, 2.f / 15.f), -1.f / 3.f), 1.f);
-  const float e = exp2f(x * (2.f * kLog2e));
+  const float e = ex2(x * (2.f * kLog2e));
   const float far = 1.f - __fdividef(2.f, 1.f + e);
   return cap * (x2 < 0.0225f ? series : far);
 }

@@ -303,9 +303,9 @@ __global__ void __launch_bounds__(32 * kDmWarps, dm_ctas(D, NT * 8)) dense_mma_k
 #pragma unroll
               for (int e = 0; e < 4; ++e) pr[e] = v[e] != v[e] ? v[e] : 0.f;
             } else {
-              corr[y] = exp2f(m[y] - mn);
+              corr[y] = ex2(m[y] - mn);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) pr[e] = exp2f(v[e] - mn);
+              for (int e = 0; e < 4; ++e) pr[e] = ex2(v[e] - mn);
             }
             m[y] = mn;
             l[y] = l[y] * corr[y] + ((pr[0] + pr[1]) + (pr[2] + pr[3]));

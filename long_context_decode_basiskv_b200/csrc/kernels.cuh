@@ -172,7 +172,8 @@ cudaError_t launch_rotary(RotaryParams p, bool bf16, int num_sms, cudaStream_t s
 
 // Attention over the whole cache: grid and scratch of one call, from the shape only.
 struct DensePlan {
-  int row_tile;  // rows (new token, head) of a tile; 0: dense_attn_mma.cu
+  int row_tile;  // rows (new token, head) of a tile; 0: dense_attn_mma.cu,
+                 // -1: dense_attn_tc.cu
   int splits;    // shares of the keys; CTAs of dense_attn_mma.cu
   size_t cnt_off, part_off, bytes;
 };
@@ -181,6 +182,8 @@ DensePlan dense_plan(int batch, int n_new, int Hq, int Hkv, int d, int r, int pa
                      int num_sms);
 void dense_plan_mma(DensePlan* pl, int batch, int rows, int Hkv, int d, int r, int page, int max_pages, int num_sms);
 cudaError_t launch_dense_mma(const DenseParams& p, cudaStream_t st);
+void dense_plan_tc(DensePlan* pl, int batch, long long rows, int Hkv, int r, int page, int max_pages, int num_sms);
+cudaError_t launch_dense_tc(const DenseParams& p, cudaStream_t st);
 cudaError_t launch_dense_attn(const DensePlan& pl, DenseParams p, bool bf16, void* scratch, cudaStream_t st);
 
 struct FuseParams {
