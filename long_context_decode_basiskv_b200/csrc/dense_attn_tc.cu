@@ -1,27 +1,34 @@
 // Attention of many new tokens over the whole paged cache (bf16, swizzled
-// rows) on the tcgen05 tensor cores: prompts, and chunks of them.
+// rows) on the tcgen05 tensor cores: prompts, chunks of them, and the few
+// tokens that dense_attn_mma.cu has too few rows for.
 //
 // One CTA per (256 rows, KV head, sequence, share of the keys): rows are
-// consecutive new tokens' G heads of the KV head, two M = 128 tiles that share
-// every key tile of 128 tokens.  Per row tile and key tile
+// consecutive new tokens' G heads of the KV head, in tiles of M = 128.  Per row
+// tile and tile of 128 keys
 //
 //   S [128 x 128] = Q [128 x d] . K^T          operands in shared memory, S in tensor memory
 //   P = 2^(S c - m), m the running row maximum   a thread owns a row: no shuffles
 //   O [128 x r]   = P [128 x 128] . C            P in tensor memory (over S), C in shared memory
 //
 // and the thread adds O to its row's fp32 accumulators, rescaled by the change
-// of the maximum.  O is not left to accumulate in tensor memory: a sum over
-// hundreds of MMAs there loses more than the fp32 result may (measured in the
-// table of the design notes), 16 MMAs do not, and adding it in registers makes
-// the rescaling one FMA that is needed anyway.  P, fp32, is multiplied as two
-// bf16 terms (hi + lo, 16 mantissa bits), like every chained product here.
+// of the maximum.  O is not left to accumulate in tensor memory: 16 MMAs add up
+// there with an error far below fp32's, hundreds would not, and adding it in
+// registers makes the rescaling one FMA that is needed anyway.  P, fp32, is
+// multiplied as two bf16 terms (hi + lo, 16 mantissa bits), like every chained
+// product of this library: o_lat is fp32 and the out-projection takes it so.
 //
-// Warps 0-3 and 4-7: softmax of the two row tiles; warps 8-11 copy K and C
-// rows from the pages into the operand layout (16-byte cp.async; rows that no
-// row of the CTA sees become zeros, so that nothing in them reaches a sum);
-// warp 12 issues the MMAs.  While one row tile is in softmax the tensor cores
-// work for the other.  Order of issue: PV(j) then S(j + 1) of a row tile, so one
-// commit tells its softmax both that O(j) can be added and that S(j + 1) is there.
+// Two softmax warpgroups, each with its own S, P and O, so that the tensor
+// cores work for one while the other is in its exponentials.  They take the two
+// row tiles of the CTA, which then share every K and C tile; where there are at
+// most 128 rows they take the even and the odd key tiles of the one row tile
+// and join at the end.  Warp 8 copies K pages (and C pages where their rows are
+// whole swizzle atoms, r a multiple of 64) by TMA straight from the paged cache:
+// the stored row swizzle is the operand's.  Warps 9-11 copy the other C tiles
+// by 16-byte cp.async: ranks that are no multiple of 64, and tiles with tokens
+// that no row of the CTA sees, which become zeros so that nothing in them
+// reaches a sum.  Warp 12 issues the MMAs.
+#include <cuda.h>
+
 #include <algorithm>
 
 #include "dense_attn.cuh"
@@ -38,35 +45,37 @@ constexpr int kDtK = 3;         // K stages
 constexpr int kDtMasks = 8;     // tiles whose page bits are kept: more than the copies run ahead
 constexpr uint32_t kDtAtom = kDtKeys * 128;  // 128 rows x 128 bytes
 
-// registers a thread: 512 x 128 at launch = 256 x 200 + 256 x 56
-constexpr int kDtRegsSoftmax = 200, kDtRegsOther = 56;
-
+// C stages, and registers of a softmax thread: 512 x 128 at launch = 256 x softmax + 256 x (256 - softmax)
 template <int RMAX> constexpr int dt_cstages() { return RMAX <= 64 ? 3 : 2; }
+template <int RMAX> constexpr int dt_regs() { return RMAX <= 64 ? 176 : RMAX <= 96 ? 200 : 208; }
 
 struct DtLayout {
   uint32_t q, k, c, bar, total;
 };
-template <int RMAX>
-__host__ __device__ constexpr DtLayout dt_layout(int d) {
+template <int D, int RMAX>
+__host__ __device__ constexpr DtLayout dt_layout() {
   DtLayout l{};
   uint32_t o = 0;
-  l.q = o; o += 2 * (uint32_t)(d / 64) * kDtAtom;
-  l.k = o; o += kDtK * (uint32_t)(d / 64) * kDtAtom;
-  l.c = o; o += dt_cstages<RMAX>() * (uint32_t)((RMAX + 63) / 64) * kDtAtom;
+  l.q = o; o += 2 * (D / 64) * kDtAtom;
+  l.k = o; o += kDtK * (D / 64) * kDtAtom;
+  l.c = o; o += dt_cstages<RMAX>() * ((RMAX + 63) / 64) * kDtAtom;
   l.bar = o; o += 256;
   l.total = o;
   return l;
 }
 
-// D += A B with A in tensor memory
-__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                          uint32_t accum) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %6, %7, %8}, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accum), "r"(0u), "r"(0u), "r"(0u), "r"(0u)
-      : "memory");
+// ---------------------------------------------------------------------------
+// tensor cores and tensor memory
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void dt_mma_ss(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, bool accum) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+               "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc),
+               "r"((uint32_t)accum) : "memory");
+}
+__device__ __forceinline__ void dt_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, bool accum) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+               "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem), "r"(a_tmem), "l"(b),
+               "r"(idesc), "r"((uint32_t)accum) : "memory");
 }
 __device__ __forceinline__ void tc_ld32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
@@ -91,20 +100,70 @@ __device__ __forceinline__ void tc_st32(uint32_t taddr, const uint32_t (&r)[32])
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// K-step j (16 elements) of a K-major swizzled operand of 128 rows
-__device__ __forceinline__ uint64_t dt_kdesc(const unsigned char* base, int j) {
-  return smem_desc_sw128(base + (size_t)(j >> 2) * kDtAtom) + (uint64_t)((j & 3) * 32 >> 4);
-}
-// K-step j (16 keys) of the C tile: the columns of a key contiguous (MN-major), 64 of them per swizzled
-// 128-byte row, 8-key groups 1024 bytes apart, 64-column atoms kDtAtom apart
-__device__ __forceinline__ uint64_t dt_cdesc(const unsigned char* base, int j) {
-  const uint64_t addr = smem_u32(base) + (uint32_t)j * 2048u;
-  return ((addr >> 4) & 0x3fffull) | ((uint64_t)(kDtAtom >> 4) << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+// the C tile as B operand: the columns of a key contiguous (MN-major), 64 of them per swizzled 128-byte
+// row, 8-key groups 1024 bytes apart, 64-column atoms kDtAtom apart
+__device__ __forceinline__ uint64_t dt_cdesc(const unsigned char* base) {
+  return ((smem_u32(base) >> 4) & 0x3fffull) | ((uint64_t)(kDtAtom >> 4) << 16) | (64ull << 32) | (1ull << 46) |
+         (2ull << 61);
 }
 
-template <int RMAX>
-__global__ void __launch_bounds__(kDtThreads, 1) dense_tc_kernel(DenseParams p) {
+// a page's rows of one 64-column half -> 128-byte rows in shared memory
+__device__ __forceinline__ void dt_tma(void* dst, const CUtensorMap* map, int half, int block, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(smem_u32(dst)), "l"(map), "r"(0), "r"(half), "r"(0), "r"(block), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// two fp32 operations in one instruction
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+  return v;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// barrier of the 96 threads of warps 9-11: whether `x` holds in all of them
+__device__ __forceinline__ bool all_of_96(bool x) {
+  uint32_t y;
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+               "barrier.cta.red.and.pred p, 2, 96, q;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(y) : "r"((uint32_t)x) : "memory");
+  return y != 0;
+}
+
+// bits [lo, hi) of a 32-bit word (bounds of any size)
+__device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
+  const uint32_t below_hi = hi >= 32 ? 0xffffffffu : hi <= 0 ? 0u : (1u << hi) - 1u;
+  const uint32_t below_lo = lo >= 32 ? 0xffffffffu : lo <= 0 ? 0u : (1u << lo) - 1u;
+  return below_hi & ~below_lo;
+}
+
+template <int D, int RMAX>
+__global__ void __launch_bounds__(kDtThreads, 1)
+    dense_tc_kernel(const __grid_constant__ DenseParams p, const __grid_constant__ CUtensorMap kmap,
+                    const __grid_constant__ CUtensorMap cmap) {
   constexpr int CS = dt_cstages<RMAX>();
+  constexpr int KA = D / 64, CA = (RMAX + 63) / 64;  // atoms of a K row, of a C row
+  constexpr bool kTwoO = RMAX <= 64;                 // room for two O of a row tile
+  constexpr uint32_t k_stage = KA * kDtAtom, c_stage = CA * kDtAtom;
+  constexpr DtLayout lay = dt_layout<D, RMAX>();
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -112,17 +171,16 @@ __global__ void __launch_bounds__(kDtThreads, 1) dense_tc_kernel(DenseParams p) 
   __shared__ int s_last;
   __shared__ uint32_t s_pages[kDtMasks];  // bit x: page x of the tile is there
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int d = p.d, r = p.r, P = p.page;
-  const DtLayout lay = dt_layout<RMAX>(d);
+  const int r = p.r, P = p.page, psh = 31 - __clz(P), np = kDtKeys >> psh;
   unsigned char* sQ = smem + lay.q;
-  const uint32_t k_stage = (uint32_t)(d / 64) * kDtAtom, c_stage = (uint32_t)((RMAX + 63) / 64) * kDtAtom;
   uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + lay.bar);
   uint64_t* kempty = kfull + kDtK;
   uint64_t* cfull = kempty + kDtK;
   uint64_t* cempty = cfull + CS;
-  uint64_t* sfull = cempty + CS;   // per row tile: S(j) there, O(j - 1) too
-  uint64_t* pfull = sfull + 2;     // per row tile: P(j) there, O(j - 1) taken
-  uint64_t* odone = pfull + 2;     // the last O of both row tiles
+  uint64_t* qfull = cempty + CS;
+  uint64_t* sfull = qfull + 1;     // per warpgroup: S there, the O before it too
+  uint64_t* pfull = sfull + 2;     // per warpgroup: P there, the O that the next PV overwrites taken
+  uint64_t* odone = pfull + 2;     // every product
 
   // this CTA's rows and keys; the last row tiles of a prompt see the most keys and start first
   const int tiles = (int)(((long long)p.n_new * p.G + kDtRows - 1) / kDtRows);
@@ -131,26 +189,30 @@ __global__ void __launch_bounds__(kDtThreads, 1) dense_tc_kernel(DenseParams p) 
   const int g = u % p.Hkv;
   u /= p.Hkv;
   const int b = u % p.batch, rt = tiles - 1 - u / p.batch;
-  const long long row0 = (long long)rt * kDtRows;
-  const int rows = (int)min((long long)kDtRows, (long long)p.n_new * p.G - row0);
-  const int mt = rows > kDtM ? 2 : 1;
+  const int row0 = rt * kDtRows;  // of the sequence: n_new G < 2^25
+  const int rows = min(kDtRows, p.n_new * p.G - row0);
+  const bool two = rows > kDtM;   // two row tiles; else two shares of the key tiles
   const DenseSeq sq = dense_seq(p, b, tid == 0 && g == 0);
   const int pos0 = sq.L - p.n_new;
-  const int t_lo = (int)(row0 / p.G), t_hi = (int)((row0 + rows - 1) / p.G);
+  const int t_lo = row0 / p.G, t_hi = (row0 + rows - 1) / p.G;
   KeyTiles kt{0, 0, 0};
   if (sq.L > 0) kt = key_tiles(pos0 + t_lo, pos0 + t_hi, sq.L, p.window, sq.prefix, kDtKeys);
   const int lo = (int)((long long)kt.count() * split / p.splits);
   const int n = (int)((long long)kt.count() * (split + 1) / p.splits) - lo;  // key tiles of this CTA
+  // keys that some row of the CTA sees: [0, prefix) and [see_lo, see_hi)
+  const int see_lo = p.window > 0 ? pos0 + t_lo - p.window + 1 : 0;
+  const int see_hi = min(sq.L, max(pos0 + t_hi + 1, sq.prefix));
 
   if (tid == 0) {
     for (int s = 0; s < kDtK; ++s) {
-      mbar_init(&kfull[s], 128);
+      mbar_init(&kfull[s], 1);
       mbar_init(&kempty[s], 1);
     }
     for (int s = 0; s < CS; ++s) {
-      mbar_init(&cfull[s], 128);
+      mbar_init(&cfull[s], 1);
       mbar_init(&cempty[s], 1);
     }
+    mbar_init(qfull, two ? 256 : 128);
     for (int m = 0; m < 2; ++m) {
       mbar_init(&sfull[m], 1);
       mbar_init(&pfull[m], 128);
@@ -158,27 +220,10 @@ __global__ void __launch_bounds__(kDtThreads, 1) dense_tc_kernel(DenseParams p) 
     mbar_init(odone, 1);
     fence_mbar_init();
   }
-  if (warp == 0) {
+  if (warp == 12) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
-  {  // the rows' queries, as the A operand
-    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q);
-    const int cpr = d / 8;
-    for (int x = tid; x < mt * kDtM * cpr; x += kDtThreads) {
-      const int row = x / cpr, c = x - row * cpr;
-      const bool valid = row < rows;
-      const long long gr = row0 + (valid ? row : 0);
-      const long long t = gr / p.G;
-      const size_t src = (((size_t)b * p.n_new + t) * p.Hq + (size_t)g * p.G + (gr - t * p.G)) * d + (size_t)c * 8;
-      unsigned char* dst = sQ + (size_t)(row / kDtM) * k_stage + (size_t)(c >> 3) * kDtAtom + (row % kDtM) * 128 +
-                           (((c & 7) ^ (row & 7)) << 4);
-      cp_async16_zfill(dst, q + src, valid);
-    }
-    cp_async_commit_group();
-    cp_async_wait_group<0>();
-    fence_proxy_async_smem();
   }
   tc_fence_before();
   __syncthreads();
@@ -188,120 +233,213 @@ __global__ void __launch_bounds__(kDtThreads, 1) dense_tc_kernel(DenseParams p) 
 
   if (warp < 8) {
     // ------------------------------------------------------------------ softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kDtRegsSoftmax));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(dt_regs<RMAX>()));
     const int m = warp >> 2;
-    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lanes + (uint32_t)m * 128, tO = tmem + lanes + 256 + (uint32_t)m * 128;
-    const int row = tid & 255;  // of the CTA
-    const bool active = m < mt;
-    const long long grow = row0 + min(row, rows - 1);
-    const int t = (int)(grow / p.G), h = g * p.G + (int)(grow - (long long)t * p.G);
+    const uint32_t tS = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)m * 128, tO = tS + 256;
+    const int row = two ? tid : tid & 127;  // of the CTA
+    const int mine = two ? n : (n + 1 - m) / 2;  // key tiles of this warpgroup
+    const int srow = row0 + min(row, rows - 1);
+    const int t = srow / p.G, h = g * p.G + srow - t * p.G;
     const int pos = pos0 + t;
-    // positions of this row tile's first and last row
-    const int i0 = pos0 + (int)((row0 + min(m * kDtM, rows - 1)) / p.G);
-    const int i1 = pos0 + (int)((row0 + min(m * kDtM + kDtM - 1, rows - 1)) / p.G);
+    if (two || m == 0) {  // the row's query, as A operand
+      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + (((size_t)b * p.n_new + t) * p.Hq + h) * D;
+      unsigned char* dst = sQ + (size_t)m * k_stage + (row & 127) * 128;
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c)
+        cp_async16_zfill(dst + (c >> 3) * kDtAtom + (((c & 7) ^ (row & 7)) << 4), q + c * 8, row < rows);
+      cp_async_commit_group();
+      cp_async_wait_group<0>();
+      fence_proxy_async_smem();
+      mbar_arrive(qfull);
+    }
+    const bool work = (row & ~31) < rows;  // this warp holds rows
+    // first and last position of the warpgroup's rows
+    const int m0 = two ? m * kDtM : 0;
+    const int i0 = pos0 + (row0 + min(m0, rows - 1)) / p.G;
+    const int i1 = pos0 + (row0 + min(m0 + kDtM - 1, rows - 1)) / p.G;
     const float slope = p.slopes ? p.slopes[h] * kLog2e : 0.f;
     const bool mod = p.cap > 0.f || p.slopes;
     const float c1 = mod ? 1.f : p.scale;
-    const uint32_t all_pages = (P == 64) ? 3u : (P == 32) ? 15u : 255u;
-    const int psh = 31 - __clz(P);
+    const uint64_t c2 = pack2(c1, c1);
     float mx = -INFINITY, l = 0.f, corr = 1.f;
     float acc[RMAX];
 #pragma unroll
     for (int c = 0; c < RMAX; ++c) acc[c] = 0.f;
 
-    auto add_o = [&]() {
+    // acc = acc cf + the O at taddr
+    auto add_o = [&](uint32_t taddr, float cf) {
+      const uint64_t cf2 = pack2(cf, cf);
 #pragma unroll
-      for (int c0 = 0; c0 < RMAX; c0 += 16) {
-        if (c0 < r) {
-          float o[16];
-          tc_ld16(tO + (uint32_t)c0, o);
+      for (int c0 = 0; c0 < RMAX; c0 += 32) {
+        if (c0 < r) {  // r is a multiple of 16: the last 32 columns may be half another O's, or unused
+          uint32_t o[32];
+          tc_ld32(taddr + (uint32_t)c0, o);
+          tc_wait_ld();
 #pragma unroll
-          for (int c = 0; c < 16; ++c) acc[c0 + c] = fmaf(acc[c0 + c], corr, o[c]);
+          for (int c = 0; c < 32; c += 2) {
+            const uint64_t v = fma2(pack2(acc[c0 + c], acc[c0 + c + 1]), cf2,
+                                    pack2(__uint_as_float(o[c]), __uint_as_float(o[c + 1])));
+            unpack2(v, acc[c0 + c], acc[c0 + c + 1]);
+          }
         }
       }
     };
 
-    for (int j = 0; active && j < n; ++j) {
+    for (int j = 0; j < mine; ++j) {
       if (!__all_sync(kFull, mbar_wait_bounded(&sfull[m], (uint32_t)(j & 1)))) {
         ok = false;
         break;
       }
       tc_fence_after();
-      if (j > 0) add_o();
-      const int j0 = kt.tile(lo + j) * kDtKeys;
-      const uint32_t pages = s_pages[j % kDtMasks];
-      const bool whole = pages == all_pages &&
-          (j0 + kDtKeys <= sq.prefix || (j0 + kDtKeys - 1 <= i0 && (p.window == 0 || i1 - j0 < p.window)));
-      float top = -INFINITY;
-      if (whole && !mod) {
+      if (work) {
+        if (!kTwoO && j > 0) add_o(tO, corr);
+        const int jt = two ? j : 2 * j + m;
+        const int j0 = kt.tile(lo + jt) * kDtKeys;
+        const uint32_t pages = s_pages[jt % kDtMasks];
+        const bool whole = pages == (1u << np) - 1u &&
+            (j0 + kDtKeys <= sq.prefix || (j0 + kDtKeys - 1 <= i0 && (p.window == 0 || i1 - j0 < p.window)));
+        float top = -INFINITY;
+        if (whole && !mod) {
+          uint32_t s[2][32];
+          tc_ld32(tS, s[0]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t s[32];
-          tc_ld32(tS + 32 * c, s);
-          tc_wait_ld();
+          for (int c = 0; c < 4; ++c) {
+            tc_wait_ld();
+            if (c < 3) tc_ld32(tS + 32 * (c + 1), s[(c + 1) & 1]);
+            float t1 = -INFINITY;
 #pragma unroll
-          for (int x = 0; x < 32; x += 2) top = fmaxf(top, fmaxf(__uint_as_float(s[x]), __uint_as_float(s[x + 1])));
-        }
-      } else {
-        // scores as they count, written back over S
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t s[32];
-          tc_ld32(tS + 32 * c, s);
-          tc_wait_ld();
-#pragma unroll
-          for (int x = 0; x < 32; ++x) {
-            const int jj = 32 * c + x, key = j0 + jj;
-            float v = __uint_as_float(s[x]);
-            if (mod) v = mod_score(v, p.scale, p.cap, slope, pos, key);
-            if (!whole && !(((pages >> (jj >> psh)) & 1u) && sees(pos, key, sq.L, p.window, sq.prefix))) v = -INFINITY;
-            top = fmaxf(top, v);
-            s[x] = __float_as_uint(v);
+            for (int x = 0; x < 32; x += 4) {
+              top = fmaxf(top, fmaxf(__uint_as_float(s[c & 1][x]), __uint_as_float(s[c & 1][x + 1])));
+              t1 = fmaxf(t1, fmaxf(__uint_as_float(s[c & 1][x + 2]), __uint_as_float(s[c & 1][x + 3])));
+            }
+            top = fmaxf(top, t1);
           }
-          tc_st32(tS + 32 * c, s);
+        } else {
+          // scores as they count, written back over S.  Seen keys of the tile, as bits: the range that the
+          // row's position and window give, and the prefix
+          const int e = min(sq.L, pos + 1) - j0, a = p.window > 0 ? pos - p.window + 1 - j0 : 0, pr = sq.prefix - j0;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t s[32];
+            tc_ld32(tS + 32 * c, s);
+            uint32_t bits = bit_range(a - 32 * c, e - 32 * c) | bit_range(0, pr - 32 * c);
+            if (P == 16) bits &= ((pages >> (2 * c) & 1u) ? 0x0000ffffu : 0u) | ((pages >> (2 * c + 1) & 1u) ? 0xffff0000u : 0u);
+            else if (!((pages >> ((32 * c) >> psh)) & 1u)) bits = 0;
+            tc_wait_ld();
+            if (p.cap > 0.f) {
+              float big = 0.f;
+#pragma unroll
+              for (int x = 0; x < 32; ++x) big = fmaxf(big, fabsf(__uint_as_float(s[x])));
+              const uint64_t sc2 = pack2(p.scale, p.scale), cap2 = pack2(p.cap, p.cap);
+              if (__any_sync(kFull, !(big * p.scale <= 1.f))) {
+#pragma unroll
+                for (int x = 0; x < 32; ++x) s[x] = __float_as_uint(cap_score(__uint_as_float(s[x]) * p.scale, p.cap));
+              } else {
+#pragma unroll
+                for (int x = 0; x < 32; x += 2) {
+                  const uint64_t v = mul2(pack2(__uint_as_float(s[x]), __uint_as_float(s[x + 1])), sc2);
+                  const uint64_t v2 = mul2(v, v);
+                  uint64_t y = pack2(tanh_coef(kTanhTop), tanh_coef(kTanhTop));
+#pragma unroll
+                  for (int k = kTanhTop - 1; k >= 0; --k) y = fma2(y, v2, pack2(tanh_coef(k), tanh_coef(k)));
+                  float y0, y1;
+                  unpack2(mul2(mul2(y, v), cap2), y0, y1);
+                  s[x] = __float_as_uint(y0);
+                  s[x + 1] = __float_as_uint(y1);
+                }
+              }
+            } else if (mod) {
+#pragma unroll
+              for (int x = 0; x < 32; ++x) s[x] = __float_as_uint(__uint_as_float(s[x]) * p.scale);
+            }
+            if (p.slopes) {
+              const float far = (float)(pos - j0 - 32 * c);
+#pragma unroll
+              for (int x = 0; x < 32; ++x)
+                s[x] = __float_as_uint(fmaf(-slope, fabsf(far - (float)x), __uint_as_float(s[x])));
+            }
+#pragma unroll
+            for (int x = 0; x < 32; ++x) {
+              const float v = (bits >> x) & 1u ? __uint_as_float(s[x]) : -INFINITY;
+              top = fmaxf(top, v);
+              s[x] = __float_as_uint(v);
+            }
+            tc_st32(tS + 32 * c, s);
+          }
           tc_wait_st();
         }
-      }
-      const float mn = fmaxf(mx, top * c1);
-      const float base = mn == -INFINITY ? 0.f : mn;  // nothing seen yet: scores are -inf or NaN, weights 0 or NaN
-      corr = mn == -INFINITY ? 1.f : ex2(mx - mn);
-      mx = mn;
-      float sum0 = 0.f, sum1 = 0.f;
+        const float mn = fmaxf(mx, top * c1);
+        const float base = mn == -INFINITY ? 0.f : mn;  // nothing seen yet: scores are -inf or NaN, weights 0 or NaN
+        const float prev = corr;
+        corr = mn == -INFINITY ? 1.f : ex2(mx - mn);
+        mx = mn;
+        const uint64_t nb = pack2(-base, -base), minus = pack2(-1.f, -1.f);
+        uint64_t sum = 0;  // (0, 0)
+        uint32_t s[2][32];
+        tc_ld32(tS, s[0]);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t s[32];
-        tc_ld32(tS + 32 * c, s);
-        tc_wait_ld();
-        uint32_t w[32];  // 16 words of hi pairs, 16 of lo pairs
+        for (int c = 0; c < 4; ++c) {
+          tc_wait_ld();
+          if (c < 3) tc_ld32(tS + 32 * (c + 1), s[(c + 1) & 1]);
+          uint32_t w[32];  // 16 words of hi pairs, 16 of lo pairs
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
-          const float a = ex2(fmaf(__uint_as_float(s[2 * x]), c1, -base));
-          const float e = ex2(fmaf(__uint_as_float(s[2 * x + 1]), c1, -base));
-          sum0 += a;
-          sum1 += e;
-          const __nv_bfloat162 hi = __floats2bfloat162_rn(a, e);
-          w[x] = *reinterpret_cast<const uint32_t*>(&hi);
-          const __nv_bfloat162 low = __floats2bfloat162_rn(a - bf16lo(w[x]), e - bf16hi(w[x]));
-          w[16 + x] = *reinterpret_cast<const uint32_t*>(&low);
+          for (int x = 0; x < 16; ++x) {
+            float a, e;
+            unpack2(fma2(pack2(__uint_as_float(s[c & 1][2 * x]), __uint_as_float(s[c & 1][2 * x + 1])), c2, nb), a, e);
+            a = ex2(a);
+            e = ex2(e);
+            const uint64_t w2 = pack2(a, e);
+            sum = add2(sum, w2);
+            const __nv_bfloat162 hi = __floats2bfloat162_rn(a, e);
+            w[x] = *reinterpret_cast<const uint32_t*>(&hi);
+            unpack2(fma2(pack2(bf16lo(w[x]), bf16hi(w[x])), minus, w2), a, e);
+            const __nv_bfloat162 low = __floats2bfloat162_rn(a, e);
+            w[16 + x] = *reinterpret_cast<const uint32_t*>(&low);
+          }
+          tc_st32(tS + 32 * c, w);
         }
-        tc_st32(tS + 32 * c, w);
-      }
-      l = fmaf(l, corr, sum0 + sum1);
-      tc_wait_st();
-      tc_fence_before();
-      mbar_arrive(&pfull[m]);
-    }
-    if (active && n > 0 && ok) {
-      if (__all_sync(kFull, mbar_wait_bounded(odone, 0))) {
-        tc_fence_after();
-        add_o();
+        float sum0, sum1;
+        unpack2(sum, sum0, sum1);
+        l = fmaf(l, corr, sum0 + sum1);
+        tc_wait_st();
+        tc_fence_before();
+        mbar_arrive(&pfull[m]);
+        // off the way of the tensor cores where there are two O: the one before this tile's
+        if (kTwoO && j > 0) add_o(tO + (uint32_t)((j - 1) & 1) * 64, prev);
       } else {
-        ok = false;
+        tc_fence_before();
+        mbar_arrive(&pfull[m]);
       }
+    }
+    if (n > 0 && ok) {
+      if (!__all_sync(kFull, mbar_wait_bounded(odone, 0))) ok = false;
+      tc_fence_after();
+      if (ok && work && mine > 0) add_o(tO + (kTwoO ? (uint32_t)((mine - 1) & 1) * 64 : 0u), corr);
     }
     if (!ok) l = __int_as_float(0x7fc00000);
-    if (active && row < rows) {
+    if (!two) {
+      // the odd key tiles' result joins the even ones'; every product is done, so the K stages are free
+      float* x = reinterpret_cast<float*>(smem + lay.k) + (row & 127);
+      if (m == 1) {
+        x[0] = mx;
+        x[128] = l;
+#pragma unroll
+        for (int c = 0; c < RMAX; ++c)
+          if (c < r) x[128 * (2 + c)] = acc[c];
+      }
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (m == 0) {
+        const float mo = x[0], lo2 = x[128];
+        const float mn = fmaxf(mx, mo);
+        const float fa = mn == -INFINITY ? 1.f : ex2(mx - mn), fb = mn == -INFINITY ? 1.f : ex2(mo - mn);
+        mx = mn;
+        l = l * fa + lo2 * fb;
+#pragma unroll
+        for (int c = 0; c < RMAX; ++c)
+          if (c < r) acc[c] = acc[c] * fa + x[128 * (2 + c)] * fb;
+      }
+    }
+    if ((two || m == 0) && row < rows) {
       if (p.splits > 1) {
         const size_t unit = blockIdx.x / p.splits;
         float* out = p.part + ((unit * p.splits + split) * kDtRows + row) * (size_t)(r + 2);
@@ -315,21 +453,14 @@ __global__ void __launch_bounds__(kDtThreads, 1) dense_tc_kernel(DenseParams p) 
 #pragma unroll
         for (int c = 0; c < RMAX; c += 4)
           if (c < r)
-            *reinterpret_cast<float4*>(p.o + at * r + c) = make_float4(acc[c] * inv, acc[c + 1] * inv, acc[c + 2] * inv, acc[c + 3] * inv);
+            *reinterpret_cast<float4*>(p.o + at * r + c) =
+                make_float4(acc[c] * inv, acc[c + 1] * inv, acc[c + 2] * inv, acc[c + 3] * inv);
         if (p.lse) p.lse[at] = l > 0.f ? (mx + log2f(l)) * kLn2 : (l == l ? -INFINITY : l);
       }
     }
-  } else if (warp < 12) {
-    // ------------------------------------------------------------------ copies
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kDtRegsOther));
-    const int ct = tid - 256;
-    const __nv_bfloat16* kr = static_cast<const __nv_bfloat16*>(p.k_raw);
-    const __nv_bfloat16* cl = static_cast<const __nv_bfloat16*>(p.c_lat);
-    const int psh = 31 - __clz(P), np = kDtKeys >> psh;
-    const int see_lo = p.window > 0 ? pos0 + t_lo - p.window + 1 : 0;
-    const int see_hi = min(sq.L, max(pos0 + t_hi + 1, sq.prefix));
-    auto seen = [&](int key) { return key < see_hi && (key >= see_lo || key < sq.prefix); };
-    // lane x < np: physical page x of tile j (-1: nothing seen there, or a bad entry)
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(256 - dt_regs<RMAX>()));
+    // physical page of lane x < np of key tile j: -1 where no row sees any of it, or for a bad entry
     auto pages_of = [&](int j) {
       int id = -1;
       if (j < n && lane < np) {
@@ -338,127 +469,158 @@ __global__ void __launch_bounds__(kDtThreads, 1) dense_tc_kernel(DenseParams p) 
       }
       return id;
     };
-    const int kc = d / 8, krow = ct / kc, kch = ct - krow * kc, kstep = 128 / kc;
-    const int cc = r / 8;
-    auto copy_k = [&](int j, int ids) {
+    // C tile j comes by TMA: whole swizzle atoms, every token seen by some row
+    auto c_by_tma = [&](int j, uint32_t bits) {
       const int j0 = kt.tile(lo + j) * kDtKeys;
-      unsigned char* dst = smem + lay.k + (size_t)(j % kDtK) * k_stage + (size_t)(kch >> 3) * kDtAtom + ((kch & 7) << 4);
-      for (int row = krow; row < kDtKeys; row += kstep) {
-        const int id = __shfl_sync(kFull, ids, row >> psh);
-        const bool valid = id >= 0 && seen(j0 + row);
-        const size_t src = valid ? (((size_t)id * p.Hkv + g) * P + (row & (P - 1))) * d + (size_t)kch * 8 : 0;
-        cp_async16_zfill(dst + row * 128, kr + src, valid);  // stored swizzle = operand swizzle
-      }
+      return r % 64 == 0 && bits == (1u << np) - 1u && j0 + kDtKeys <= see_hi &&
+             (j0 >= see_lo || j0 + kDtKeys <= sq.prefix);
     };
-    auto copy_c = [&](int j, int ids) {
-      const int j0 = kt.tile(lo + j) * kDtKeys;
-      unsigned char* dst = smem + lay.c + (size_t)(j % CS) * c_stage;
-      const int dr = 128 / cc, dc = 128 - dr * cc;
-      int row = ct / cc, ch = ct - row * cc;
-      for (int x = 0; x < cc; ++x) {
-        const int id = __shfl_sync(kFull, ids, row >> psh);
-        const bool valid = id >= 0 && seen(j0 + row);
-        const size_t src = valid ? (((size_t)id * p.Hkv + g) * P + (row & (P - 1))) * r + (size_t)ch * 8 : 0;
-        const int c = ch ^ (row & p.mc);  // the chunk that is stored here
-        cp_async16_zfill(dst + (size_t)(c >> 3) * kDtAtom + row * 128 + (((c & 7) ^ (row & 7)) << 4), cl + src, valid);
-        row += dr;
-        ch += dc;
-        if (ch >= cc) {
-          ch -= cc;
-          ++row;
+    if (warp == 8) {
+      // ---------------------------------------------------------------- copies by TMA
+      int ids = pages_of(0), ids_c = -1;
+      uint32_t bits_c = 0;
+      int issued = 0, last_c = -1;  // K tiles issued, the last C tile issued here
+      for (int j = 0; j <= n && ok; ++j) {
+        const int next = pages_of(j + 1);
+        const uint32_t bits = __ballot_sync(kFull, ids >= 0);
+        if (j < n) {
+          const int s = j % kDtK;
+          if (j >= kDtK && !__all_sync(kFull, mbar_wait_bounded(&kempty[s], (uint32_t)((j / kDtK - 1) & 1)))) {
+            ok = false;
+            break;
+          }
+          issued = j + 1;
+          if (lane == 0) {
+            s_pages[j % kDtMasks] = bits;
+            mbar_arrive_expect_tx(&kfull[s], (uint32_t)__popc(bits) * P * D * 2);
+          }
+          __syncwarp();
+          if (ids >= 0) {
+#pragma unroll
+            for (int a = 0; a < KA; ++a)
+              dt_tma(smem + lay.k + (size_t)s * k_stage + a * kDtAtom + ((lane * 128) << psh), &kmap, a,
+                     ids * p.Hkv + g, &kfull[s]);
+          }
         }
-      }
-    };
-    // groups in the order K(0), [K(1), C(0)], [K(2), C(1)] ...: a pair is told to the MMA warp when the
-    // next pair has been issued, so that two tiles are always in flight
-    int ids_k = pages_of(0), ids_c = -1;
-    for (int j = 0; j <= n && ok; ++j) {
-      const int ids_next = pages_of(j + 1);
-      if (j < n) {
-        if (j >= kDtK && !__all_sync(kFull, mbar_wait_bounded(&kempty[j % kDtK], (uint32_t)((j / kDtK - 1) & 1)))) {
+        // (each role waits for every tile's stage, its own or not: a parity says nothing two phases on)
+        if (j - 1 >= CS &&
+            !__all_sync(kFull, mbar_wait_bounded(&cempty[(j - 1) % CS], (uint32_t)(((j - 1) / CS - 1) & 1)))) {
           ok = false;
           break;
         }
-        if (warp == 8) {
-          const uint32_t bits = __ballot_sync(kFull, ids_k >= 0);
-          if (lane == 0) s_pages[j % kDtMasks] = bits;
+        if (j > 0 && c_by_tma(j - 1, bits_c)) {
+          const int s = (j - 1) % CS;
+          last_c = j - 1;
+          if (lane == 0) mbar_arrive_expect_tx(&cfull[s], (uint32_t)kDtKeys * r * 2);
+          __syncwarp();
+          if (ids_c >= 0)
+            for (int a = 0; a < r / 64; ++a)
+              dt_tma(smem + lay.c + (size_t)s * c_stage + a * kDtAtom + ((lane * 128) << psh), &cmap, a,
+                     ids_c * p.Hkv + g, &cfull[s]);
         }
-        __syncwarp();
-        copy_k(j, ids_k);
+        ids_c = ids;
+        bits_c = bits;
+        ids = next;
       }
-      cp_async_commit_group();
-      if (j > 0) {
-        if (j - 1 >= CS && !__all_sync(kFull, mbar_wait_bounded(&cempty[(j - 1) % CS], (uint32_t)(((j - 1) / CS - 1) & 1)))) {
-          ok = false;
-          break;
+      // no copy is on its way when the CTA ends, whatever became of the other warps
+      for (int j = max(0, issued - kDtK); j < issued; ++j) mbar_wait_bounded(&kfull[j % kDtK], (uint32_t)((j / kDtK) & 1));
+      // (a C stage that a later tile took was read, so its copy had landed)
+      for (int j = max(0, (ok ? n : last_c + 1) - CS); j <= last_c; ++j)
+        mbar_wait_bounded(&cfull[j % CS], (uint32_t)((j / CS) & 1));
+    } else if (warp < 12) {
+      // ---------------------------------------------------------------- the other C tiles, by 96 threads
+      const int ct = tid - 288, cc = r / 8;
+      const __nv_bfloat16* cl = static_cast<const __nv_bfloat16*>(p.c_lat);
+      const int dr = 96 / cc, dc = 96 - dr * cc;
+      int ids = pages_of(0);
+      for (int j = 0; j < n && ok; ++j) {
+        const int next = pages_of(j + 1);
+        const uint32_t bits = __ballot_sync(kFull, ids >= 0);
+        const int s = j % CS;
+        if (j >= CS) {
+          ok = all_of_96(mbar_wait_bounded(&cempty[s], (uint32_t)((j / CS - 1) & 1)));  // the three warps give up together
+          if (!ok) break;
         }
-        copy_c(j - 1, ids_c);
+        if (!c_by_tma(j, bits)) {
+          const int j0 = kt.tile(lo + j) * kDtKeys;
+          unsigned char* dst = smem + lay.c + (size_t)s * c_stage;
+          int row = ct / cc, ch = ct - row * cc;
+#pragma unroll 4
+          for (int x = ct; x < kDtKeys * cc + (96 - kDtKeys * cc % 96) % 96; x += 96) {
+            const int id = __shfl_sync(kFull, ids, min(row, kDtKeys - 1) >> psh);
+            if (row < kDtKeys) {
+              const int key = j0 + row;
+              const bool valid = id >= 0 && key < see_hi && (key >= see_lo || key < sq.prefix);
+              const size_t src = valid ? (((size_t)id * p.Hkv + g) * P + (row & (P - 1))) * r + (size_t)ch * 8 : 0;
+              const int c = ch ^ (row & p.mc);  // the chunk that is stored here
+              cp_async16_zfill(dst + (c >> 3) * kDtAtom + row * 128 + (((c & 7) ^ (row & 7)) << 4), cl + src, valid);
+            }
+            row += dr;
+            ch += dc;
+            if (ch >= cc) {
+              ch -= cc;
+              ++row;
+            }
+          }
+          cp_async_commit_group();
+          cp_async_wait_group<0>();
+          fence_proxy_async_smem();
+          all_of_96(true);
+          if (ct == 0) mbar_arrive(&cfull[s]);
+        }
+        ids = next;
       }
-      cp_async_commit_group();
-      cp_async_wait_group<2>();  // K(j - 1) and C(j - 2) are there
-      fence_proxy_async_smem();
-      if (j >= 1) mbar_arrive(&kfull[(j - 1) % kDtK]);
-      if (j >= 2) mbar_arrive(&cfull[(j - 2) % CS]);
-      ids_c = ids_k;
-      ids_k = ids_next;
-    }
-    cp_async_wait_group<0>();
-    if (ok && n > 0) {
-      fence_proxy_async_smem();
-      mbar_arrive(&cfull[(n - 1) % CS]);
-    }
-  } else {
-    // ------------------------------------------------------------------ MMA
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kDtRegsOther));
-    if (warp == 12 && lane == 0 && n > 0) {
+    } else if (warp == 12 && lane == 0 && n > 0) {
+      // ---------------------------------------------------------------- MMA
       const uint32_t id_s = idesc_bf16(kDtM, kDtKeys);
       const uint32_t id_o = idesc_bf16(kDtM, r) | (1u << 16);  // B with its columns contiguous
-      const int ks = d / 16;
-      auto scores = [&](int m, int j) {
-        const unsigned char* a = sQ + (size_t)m * k_stage;
-        const unsigned char* bb = smem + lay.k + (size_t)(j % kDtK) * k_stage;
-        for (int x = 0; x < ks; ++x)
-          tc_mma(tmem + (uint32_t)m * 128, dt_kdesc(a, x), dt_kdesc(bb, x), id_s, x > 0 ? 1u : 0u);
-      };
-      auto values = [&](int m, int j) {
-        const unsigned char* bb = smem + lay.c + (size_t)(j % CS) * c_stage;
-        const uint32_t o = tmem + 256 + (uint32_t)m * 128, pa = tmem + (uint32_t)m * 128;
-        for (int x = 0; x < kDtKeys / 16; ++x) {
-          const uint32_t at = pa + (uint32_t)(x >> 1) * 32 + (uint32_t)(x & 1) * 8;
-          tc_mma_ts(o, at, dt_cdesc(bb, x), id_o, x > 0 ? 1u : 0u);
-          tc_mma_ts(o, at + 16, dt_cdesc(bb, x), id_o, 1u);
-        }
-      };
-      for (int j = 0; j <= n && ok; ++j) {
-        // S(j) once K(j) is there; before it, the products of tile j - 1
-        if (j < n && !mbar_wait_bounded(&kfull[j % kDtK], (uint32_t)((j / kDtK) & 1))) {
-          ok = false;
-          break;
-        }
-        if (j > 0 && !mbar_wait_bounded(&cfull[(j - 1) % CS], (uint32_t)(((j - 1) / CS) & 1))) {
-          ok = false;
-          break;
-        }
-        for (int m = 0; m < mt; ++m) {
-          if (j > 0) {
-            if (!mbar_wait_bounded(&pfull[m], (uint32_t)((j - 1) & 1))) {
-          ok = false;
-          break;
-        }
+      const uint64_t qdesc = smem_desc_sw128(sQ), kdesc = smem_desc_sw128(smem + lay.k), cdesc = dt_cdesc(smem + lay.c);
+      ok = mbar_wait_bounded(qfull, 0);
+      const int steps = two ? n : (n + 1) / 2;
+      for (int j = 0; j <= steps && ok; ++j) {
+#pragma unroll 1
+        for (int m = 0; m < 2; ++m) {
+          const int tp = two ? j - 1 : 2 * (j - 1) + m, tc = two ? j : 2 * j + m;  // key tiles of PV, of S
+          const bool first = !two || m == 0, last = !two || m == 1;  // the tile's first and last use
+          if (j > 0 && tp < n) {
+            const int s = tp % CS;
+            if ((first && !mbar_wait_bounded(&cfull[s], (uint32_t)((tp / CS) & 1))) ||
+                !mbar_wait_bounded(&pfull[m], (uint32_t)((j - 1) & 1))) {
+              ok = false;
+              break;
+            }
             tc_fence_after();
-            values(m, j - 1);
+            const uint64_t bd = cdesc + (uint64_t)((uint32_t)s * c_stage >> 4);
+            const uint32_t o = tmem + 256 + (uint32_t)m * 128 + (kTwoO ? (uint32_t)((j - 1) & 1) * 64 : 0u);
+            const uint32_t pa = tmem + (uint32_t)m * 128;
+#pragma unroll
+            for (int x = 0; x < kDtKeys / 16; ++x) {
+              const uint32_t at = pa + (x >> 1) * 32 + (x & 1) * 8;
+              dt_mma_ts(o, at, bd + x * 128, id_o, x > 0);
+              dt_mma_ts(o, at + 16, bd + x * 128, id_o, true);
+            }
+            if (last) tc_commit(&cempty[s]);
           }
-          if (j < n) {
+          if (tc < n) {
+            const int s = tc % kDtK;
+            if (first && !mbar_wait_bounded(&kfull[s], (uint32_t)((tc / kDtK) & 1))) {
+              ok = false;
+              break;
+            }
             tc_fence_after();
-            scores(m, j);
+            const uint64_t ad = qdesc + (uint64_t)(two ? ((uint32_t)m * k_stage >> 4) : 0u);
+            const uint64_t bd = kdesc + (uint64_t)((uint32_t)s * k_stage >> 4);
+#pragma unroll
+            for (int x = 0; x < D / 16; ++x) {
+              const uint64_t step = (uint64_t)(((x >> 2) * kDtAtom + (x & 3) * 32) >> 4);
+              dt_mma_ss(tmem + (uint32_t)m * 128, ad + step, bd + step, id_s, x > 0);
+            }
             tc_commit(&sfull[m]);
+            if (last) tc_commit(&kempty[s]);
           }
         }
-        if (!ok) break;
-        if (j > 0) tc_commit(&cempty[(j - 1) % CS]);
-        if (j < n) tc_commit(&kempty[j % kDtK]);
       }
-      // with every product issued this covers the last of them; after a failed wait, what was issued
+      // every product, or after a failed wait what was issued
       tc_commit(odone);
       if (!mbar_wait_bounded(odone, 0)) ok = false;
     }
@@ -466,7 +628,7 @@ __global__ void __launch_bounds__(kDtThreads, 1) dense_tc_kernel(DenseParams p) 
   if (!ok) set_err(p.err, BASISKV_DEVERR_TIMEOUT);
   tc_fence_before();
   __syncthreads();
-  if (warp == 0) {
+  if (warp == 12) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
   }
@@ -475,8 +637,8 @@ __global__ void __launch_bounds__(kDtThreads, 1) dense_tc_kernel(DenseParams p) 
   if (!dense_last_split(p.cnt + unit, p.splits, p.err, &s_last)) return;
   const size_t stride = (size_t)kDtRows * (r + 2);
   for (int row = warp; row < rows; row += kDtThreads / 32) {
-    const long long gr = row0 + row, t = gr / p.G;
-    const size_t at = ((size_t)b * p.n_new + t) * p.Hq + (size_t)g * p.G + (gr - t * p.G);
+    const int sr = row0 + row, t = sr / p.G;
+    const size_t at = ((size_t)b * p.n_new + t) * p.Hq + (size_t)g * p.G + (sr - t * p.G);
     dense_join_row(p.part + unit * p.splits * stride + (size_t)row * (r + 2), stride, p.splits, r, p.o + at * r,
                    p.lse ? p.lse + at : nullptr, lane, false);
   }
@@ -493,18 +655,57 @@ void dense_plan_tc(DensePlan* pl, int batch, long long rows, int Hkv, int r, int
   if (pl->splits > 1) pl->bytes += ((size_t)units * pl->splits * kDtRows * (r + 2) * 4 + 255) & ~(size_t)255;
 }
 
-template <int RMAX>
+// ---------------------------------------------------------------------------
+// launch
+// ---------------------------------------------------------------------------
+// The driver's tensor-map encoder, looked up through the runtime (the library does not link libcuda).
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+static EncodeTiled encode_tiled() {
+  static const EncodeTiled fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeTiled>(f);
+  }();
+  return fn;
+}
+
+// [blocks][P][cols] bf16 pages (a block: one KV head of a physical page) as (64 columns, halves, rows, blocks),
+// copied a half of a block at a time; no swizzle: the rows are stored swizzled
+static cudaError_t page_map(CUtensorMap* map, const void* base, int cols, int page, long long blocks) {
+  const EncodeTiled enc = encode_tiled();
+  if (!enc) return cudaErrorNotSupported;
+  const cuuint64_t dims[4] = {64, (cuuint64_t)(cols / 64), (cuuint64_t)page, (cuuint64_t)blocks};
+  const cuuint64_t strides[3] = {128, (cuuint64_t)cols * 2, (cuuint64_t)cols * 2 * page};
+  const cuuint32_t box[4] = {64, 1, (cuuint32_t)page, 1}, one[4] = {1, 1, 1, 1};
+  const CUresult e = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, one,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return e == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int D, int RMAX>
 static cudaError_t launch_dt(const DenseParams& p, cudaStream_t st) {
-  const size_t smem = dt_layout<RMAX>(p.d).total + 1024;
-  cudaError_t e = ensure_smem((const void*)dense_tc_kernel<RMAX>, smem);
+  constexpr size_t smem = dt_layout<D, RMAX>().total + 1024;
+  static_assert(smem <= 227 * 1024, "shared memory of a CTA");
+  cudaError_t e = ensure_smem((const void*)dense_tc_kernel<D, RMAX>, smem);
   if (e != cudaSuccess) return e;
+  CUtensorMap kmap{}, cmap{};
+  const long long blocks = (long long)p.num_phys * p.Hkv;
+  if ((e = page_map(&kmap, p.k_raw, D, p.page, blocks)) != cudaSuccess) return e;
+  if (p.r % 64 == 0 && (e = page_map(&cmap, p.c_lat, p.r, p.page, blocks)) != cudaSuccess) return e;
   const long long units = ((long long)p.n_new * p.G + kDtRows - 1) / kDtRows * p.Hkv * p.batch;
-  dense_tc_kernel<RMAX><<<(unsigned)(units * p.splits), kDtThreads, smem, st>>>(p);
+  dense_tc_kernel<D, RMAX><<<(unsigned)(units * p.splits), kDtThreads, smem, st>>>(p, kmap, cmap);
   return cudaGetLastError();
 }
 
 cudaError_t launch_dense_tc(const DenseParams& p, cudaStream_t st) {
-  return p.r <= 64 ? launch_dt<64>(p, st) : launch_dt<128>(p, st);
+  if (p.d == 64) return launch_dt<64, 64>(p, st);
+  return p.r <= 64 ? launch_dt<128, 64>(p, st) : p.r <= 96 ? launch_dt<128, 96>(p, st) : launch_dt<128, 128>(p, st);
 }
 
 }  // namespace bkv
