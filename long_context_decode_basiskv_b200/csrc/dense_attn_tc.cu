@@ -43,11 +43,14 @@ constexpr int kDtKeys = 128;    // keys per tile
 constexpr int kDtThreads = 512; // 4 warpgroups: softmax, softmax, copies, MMA (one warp of it)
 constexpr int kDtK = 3;         // K stages
 constexpr int kDtMasks = 8;     // tiles whose page bits are kept: more than the copies run ahead
+constexpr int kDtDrain = 2;      // tiles whose products add up in tensor memory
+constexpr float kDtAhead = 8.f;  // a reference is this far below a row's largest score at most, in a masked or modified
+constexpr float kDtMost = 65536.f; // tile; and the sum of 32 weights of a tile seen whole is at most this
 constexpr uint32_t kDtAtom = kDtKeys * 128;  // 128 rows x 128 bytes
 
 // C stages, and registers of a softmax thread: 512 x 128 at launch = 256 x softmax + 256 x (256 - softmax)
 template <int RMAX> constexpr int dt_cstages() { return RMAX <= 64 ? 3 : 2; }
-template <int RMAX> constexpr int dt_regs() { return RMAX <= 64 ? 176 : RMAX <= 96 ? 200 : 208; }
+template <int RMAX> constexpr int dt_regs() { return RMAX <= 64 ? 192 : RMAX <= 96 ? 200 : 216; }
 
 struct DtLayout {
   uint32_t q, k, c, bar, total;
@@ -67,15 +70,29 @@ __host__ __device__ constexpr DtLayout dt_layout() {
 // ---------------------------------------------------------------------------
 // tensor cores and tensor memory
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void dt_mma_ss(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, bool accum) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-               "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc),
-               "r"((uint32_t)accum) : "memory");
+// Issued by a whole warp, for which `leader` is set in one lane: the warp stays converged, so that the
+// descriptors are formed in uniform registers (inside a one-lane branch each MMA took 70 to 100 cycles to issue).
+__device__ __forceinline__ uint32_t elect_leader() {
+  uint32_t x;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(x));
+  return x;
 }
-__device__ __forceinline__ void dt_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, bool accum) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-               "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem), "r"(a_tmem), "l"(b),
-               "r"(idesc), "r"((uint32_t)accum) : "memory");
+__device__ __forceinline__ void dt_mma_ss(uint32_t leader, uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
+                                          bool accum) {
+  asm volatile("{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+               "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem), "l"(a), "l"(b),
+               "r"(idesc), "r"((uint32_t)accum), "r"(leader) : "memory");
+}
+__device__ __forceinline__ void dt_mma_ts(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                          bool accum) {
+  asm volatile("{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+               "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem), "r"(a_tmem), "l"(b),
+               "r"(idesc), "r"((uint32_t)accum), "r"(leader) : "memory");
+}
+__device__ __forceinline__ void dt_commit(uint32_t leader, uint64_t* bar) {
+  asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+               "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+               "r"(leader) : "memory");
 }
 __device__ __forceinline__ void tc_ld32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
@@ -97,7 +114,31 @@ __device__ __forceinline__ void tc_st32(uint32_t taddr, const uint32_t (&r)[32])
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+// 8 columns of hi pairs and the 8 of their lo pairs, 16 columns on
+__device__ __forceinline__ void tc_ld16u(uint32_t taddr, uint32_t (&r)[16]) {
+#pragma unroll
+  for (int h = 0; h < 16; h += 8)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[h]), "=r"(r[h + 1]), "=r"(r[h + 2]), "=r"(r[h + 3]), "=r"(r[h + 4]), "=r"(r[h + 5]),
+                   "=r"(r[h + 6]), "=r"(r[h + 7])
+                 : "r"(taddr + 2 * h));
+}
+__device__ __forceinline__ void tc_st16u(uint32_t taddr, const uint32_t (&r)[16]) {
+#pragma unroll
+  for (int h = 0; h < 16; h += 8)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr + 2 * h),
+                 "r"(r[h]), "r"(r[h + 1]), "r"(r[h + 2]), "r"(r[h + 3]), "r"(r[h + 4]), "r"(r[h + 5]), "r"(r[h + 6]),
+                 "r"(r[h + 7])
+                 : "memory");
+}
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_st16(uint32_t taddr, const float (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};" ::"r"(taddr), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
+      "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+      : "memory");
+}
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // the C tile as B operand: the columns of a key contiguous (MN-major), 64 of them per swizzled 128-byte
@@ -140,6 +181,28 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return d;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
+  float a = __uint_as_float(s[0]), b = __uint_as_float(s[1]);
+#pragma unroll
+  for (int x = 2; x < 32; x += 4) {
+    a = max3(a, __uint_as_float(s[x]), __uint_as_float(s[x + 1]));
+    if (x + 2 < 32) b = max3(b, __uint_as_float(s[x + 2]), __uint_as_float(s[x + 3]));
+  }
+  return fmaxf(a, b);
+}
+// two fp32 values as a bf16 pair, and what it leaves of them as another
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  const __nv_bfloat162 l = __floats2bfloat162_rn(a - bf16lo(hi), b - bf16hi(hi));
+  lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+
 // barrier of the 96 threads of warps 9-11: whether `x` holds in all of them
 __device__ __forceinline__ bool all_of_96(bool x) {
   uint32_t y;
@@ -155,13 +218,15 @@ __device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
   return below_hi & ~below_lo;
 }
 
-template <int D, int RMAX>
+// MOD: scores are capped or biased
+template <int D, int RMAX, bool MOD>
 __global__ void __launch_bounds__(kDtThreads, 1)
     dense_tc_kernel(const __grid_constant__ DenseParams p, const __grid_constant__ CUtensorMap kmap,
                     const __grid_constant__ CUtensorMap cmap) {
   constexpr int CS = dt_cstages<RMAX>();
   constexpr int KA = D / 64, CA = (RMAX + 63) / 64;  // atoms of a K row, of a C row
-  constexpr bool kTwoO = RMAX <= 64;                 // room for two O of a row tile
+  constexpr int NB = RMAX <= 64 ? 3 : 2;             // S buffers: what 512 columns hold beside two O
+  constexpr uint32_t tO0 = NB * 128, tOstep = NB == 3 ? 64 : 128;
   constexpr uint32_t k_stage = KA * kDtAtom, c_stage = CA * kDtAtom;
   constexpr DtLayout lay = dt_layout<D, RMAX>();
   extern __shared__ unsigned char smem_raw[];
@@ -178,9 +243,10 @@ __global__ void __launch_bounds__(kDtThreads, 1)
   uint64_t* cfull = kempty + kDtK;
   uint64_t* cempty = cfull + CS;
   uint64_t* qfull = cempty + CS;
-  uint64_t* sfull = qfull + 1;     // per warpgroup: S there, the O before it too
-  uint64_t* pfull = sfull + 2;     // per warpgroup: P there, the O that the next PV overwrites taken
-  uint64_t* odone = pfull + 2;     // every product
+  uint64_t* sfull = qfull + 1;     // per S buffer: S there
+  uint64_t* pfull = sfull + NB;    // per S buffer: P there, and the O that its product overwrites taken
+  uint64_t* ofull = pfull + NB;    // per warpgroup: O there
+  uint64_t* odone = ofull + 2;     // every product
 
   // this CTA's rows and keys; the last row tiles of a prompt see the most keys and start first
   const int tiles = (int)(((long long)p.n_new * p.G + kDtRows - 1) / kDtRows);
@@ -213,10 +279,12 @@ __global__ void __launch_bounds__(kDtThreads, 1)
       mbar_init(&cempty[s], 1);
     }
     mbar_init(qfull, two ? 256 : 128);
-    for (int m = 0; m < 2; ++m) {
-      mbar_init(&sfull[m], 1);
-      mbar_init(&pfull[m], 128);
+    for (int x = 0; x < NB; ++x) {
+      mbar_init(&sfull[x], 1);
+      mbar_init(&pfull[x], 128);
     }
+    mbar_init(&ofull[0], 1);
+    mbar_init(&ofull[1], 1);
     mbar_init(odone, 1);
     fence_mbar_init();
   }
@@ -235,7 +303,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
     // ------------------------------------------------------------------ softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(dt_regs<RMAX>()));
     const int m = warp >> 2;
-    const uint32_t tS = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)m * 128, tO = tS + 256;
+    const uint32_t tw = tmem + ((uint32_t)((warp & 3) * 32) << 16), tO = tw + tO0 + (uint32_t)m * tOstep;
     const int row = two ? tid : tid & 127;  // of the CTA
     const int mine = two ? n : (n + 1 - m) / 2;  // key tiles of this warpgroup
     const int srow = row0 + min(row, rows - 1);
@@ -258,65 +326,81 @@ __global__ void __launch_bounds__(kDtThreads, 1)
     const int i0 = pos0 + (row0 + min(m0, rows - 1)) / p.G;
     const int i1 = pos0 + (row0 + min(m0 + kDtM - 1, rows - 1)) / p.G;
     const float slope = p.slopes ? p.slopes[h] * kLog2e : 0.f;
-    const bool mod = p.cap > 0.f || p.slopes;
-    const float c1 = mod ? 1.f : p.scale;
+    const float c1 = MOD ? 1.f : p.scale;
     const uint64_t c2 = pack2(c1, c1);
-    float mx = -INFINITY, l = 0.f, corr = 1.f;
+    // Weights are 2^(s - ref) (log 2 units).  Any reference is right that keeps them in range, so ref is a
+    // maximum that is brought up to date only when a score passes it by kDtAhead: the rescaling of l, acc
+    // and O that goes with it is rare, and tiles that are seen whole need no pass for their maximum.
+    float ref = -INFINITY, l = 0.f;
     float acc[RMAX];
 #pragma unroll
     for (int c = 0; c < RMAX; ++c) acc[c] = 0.f;
 
-    // acc = acc cf + the O at taddr
-    auto add_o = [&](uint32_t taddr, float cf) {
-      const uint64_t cf2 = pack2(cf, cf);
+    // acc += O
+    auto add_o = [&]() {
 #pragma unroll
       for (int c0 = 0; c0 < RMAX; c0 += 32) {
-        if (c0 < r) {  // r is a multiple of 16: the last 32 columns may be half another O's, or unused
+        if (c0 < r) {  // r is a multiple of 16: the last 16 of 32 columns may be unused
           uint32_t o[32];
-          tc_ld32(taddr + (uint32_t)c0, o);
+          tc_ld32(tO + (uint32_t)c0, o);
           tc_wait_ld();
 #pragma unroll
           for (int c = 0; c < 32; c += 2) {
-            const uint64_t v = fma2(pack2(acc[c0 + c], acc[c0 + c + 1]), cf2,
+            const uint64_t v = add2(pack2(acc[c0 + c], acc[c0 + c + 1]),
                                     pack2(__uint_as_float(o[c]), __uint_as_float(o[c + 1])));
             unpack2(v, acc[c0 + c], acc[c0 + c + 1]);
           }
         }
       }
     };
+    auto o_there = [&](int j) {  // the product of this warpgroup's tile j is in O
+      const bool there = __all_sync(kFull, mbar_wait_bounded(&ofull[m], (uint32_t)(j & 1)));
+      tc_fence_after();
+      return there;
+    };
 
     for (int j = 0; j < mine; ++j) {
-      if (!__all_sync(kFull, mbar_wait_bounded(&sfull[m], (uint32_t)(j & 1)))) {
+      const int x = 2 * j + m;  // the item: S buffer x % NB, for the x / NB th time
+      const uint32_t tS = tw + (uint32_t)(x % NB) * 128;
+      if (!__all_sync(kFull, mbar_wait_bounded(&sfull[x % NB], (uint32_t)((x / NB) & 1)))) {
         ok = false;
         break;
       }
       tc_fence_after();
       if (work) {
-        if (!kTwoO && j > 0) add_o(tO, corr);
-        const int jt = two ? j : 2 * j + m;
+        uint32_t sa[32];
+        tc_ld32(tS, sa);
+        const int jt = two ? j : x;
         const int j0 = kt.tile(lo + jt) * kDtKeys;
         const uint32_t pages = s_pages[jt % kDtMasks];
         const bool whole = pages == (1u << np) - 1u &&
             (j0 + kDtKeys <= sq.prefix || (j0 + kDtKeys - 1 <= i0 && (p.window == 0 || i1 - j0 < p.window)));
-        float top = -INFINITY;
-        if (whole && !mod) {
-          uint32_t s[2][32];
-          tc_ld32(tS, s[0]);
+        // A new reference: f takes what was summed relative to the old one to it.  O of the tiles since the
+        // last one that went to acc is rescaled where it is.
+        auto rebase = [&](float nref) {
+          const float f = ref == -INFINITY ? 1.f : ex2(ref - nref);  // nothing summed yet, or only NaN
+          ref = nref;
+          l *= f;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            tc_wait_ld();
-            if (c < 3) tc_ld32(tS + 32 * (c + 1), s[(c + 1) & 1]);
-            float t1 = -INFINITY;
+          for (int c = 0; c < RMAX; ++c) acc[c] *= f;
+          if (j > 0) {
+            if (!o_there(j - 1)) ok = false;
+#pragma unroll 1
+            for (int c0 = 0; c0 < r; c0 += 16) {
+              float o[16];
+              tc_ld16(tO + (uint32_t)c0, o);
 #pragma unroll
-            for (int x = 0; x < 32; x += 4) {
-              top = fmaxf(top, fmaxf(__uint_as_float(s[c & 1][x]), __uint_as_float(s[c & 1][x + 1])));
-              t1 = fmaxf(t1, fmaxf(__uint_as_float(s[c & 1][x + 2]), __uint_as_float(s[c & 1][x + 3])));
+              for (int c = 0; c < 16; ++c) o[c] *= f;
+              tc_st16(tO + (uint32_t)c0, o);
             }
-            top = fmaxf(top, t1);
+            tc_wait_st();
           }
-        } else {
-          // scores as they count, written back over S.  Seen keys of the tile, as bits: the range that the
-          // row's position and window give, and the prefix
+          return f;
+        };
+        if (MOD || !whole || __any_sync(kFull, ref == -INFINITY)) {
+          // scores as they count, written back over S, and their maximum.  Seen keys of the tile, as bits:
+          // the range that the row's position and window give, and the prefix
+          float top = -INFINITY;
           const int e = min(sq.L, pos + 1) - j0, a = p.window > 0 ? pos - p.window + 1 - j0 : 0, pr = sq.prefix - j0;
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
@@ -326,96 +410,137 @@ __global__ void __launch_bounds__(kDtThreads, 1)
             if (P == 16) bits &= ((pages >> (2 * c) & 1u) ? 0x0000ffffu : 0u) | ((pages >> (2 * c + 1) & 1u) ? 0xffff0000u : 0u);
             else if (!((pages >> ((32 * c) >> psh)) & 1u)) bits = 0;
             tc_wait_ld();
-            if (p.cap > 0.f) {
+            if (MOD && p.cap > 0.f) {
               float big = 0.f;
 #pragma unroll
-              for (int x = 0; x < 32; ++x) big = fmaxf(big, fabsf(__uint_as_float(s[x])));
+              for (int y = 0; y < 32; ++y) big = fmaxf(big, fabsf(__uint_as_float(s[y])));
               const uint64_t sc2 = pack2(p.scale, p.scale), cap2 = pack2(p.cap, p.cap);
               if (__any_sync(kFull, !(big * p.scale <= 1.f))) {
 #pragma unroll
-                for (int x = 0; x < 32; ++x) s[x] = __float_as_uint(cap_score(__uint_as_float(s[x]) * p.scale, p.cap));
+                for (int y = 0; y < 32; ++y) s[y] = __float_as_uint(cap_score(__uint_as_float(s[y]) * p.scale, p.cap));
               } else {
 #pragma unroll
-                for (int x = 0; x < 32; x += 2) {
-                  const uint64_t v = mul2(pack2(__uint_as_float(s[x]), __uint_as_float(s[x + 1])), sc2);
+                for (int y = 0; y < 32; y += 2) {
+                  const uint64_t v = mul2(pack2(__uint_as_float(s[y]), __uint_as_float(s[y + 1])), sc2);
                   const uint64_t v2 = mul2(v, v);
-                  uint64_t y = pack2(tanh_coef(kTanhTop), tanh_coef(kTanhTop));
+                  uint64_t t2 = pack2(tanh_coef(kTanhTop), tanh_coef(kTanhTop));
 #pragma unroll
-                  for (int k = kTanhTop - 1; k >= 0; --k) y = fma2(y, v2, pack2(tanh_coef(k), tanh_coef(k)));
+                  for (int k = kTanhTop - 1; k >= 0; --k) t2 = fma2(t2, v2, pack2(tanh_coef(k), tanh_coef(k)));
                   float y0, y1;
-                  unpack2(mul2(mul2(y, v), cap2), y0, y1);
-                  s[x] = __float_as_uint(y0);
-                  s[x + 1] = __float_as_uint(y1);
+                  unpack2(mul2(mul2(t2, v), cap2), y0, y1);
+                  s[y] = __float_as_uint(y0);
+                  s[y + 1] = __float_as_uint(y1);
                 }
               }
-            } else if (mod) {
+            } else if (MOD) {
 #pragma unroll
-              for (int x = 0; x < 32; ++x) s[x] = __float_as_uint(__uint_as_float(s[x]) * p.scale);
+              for (int y = 0; y < 32; ++y) s[y] = __float_as_uint(__uint_as_float(s[y]) * p.scale);
             }
-            if (p.slopes) {
+            if (MOD && p.slopes) {
               const float far = (float)(pos - j0 - 32 * c);
 #pragma unroll
-              for (int x = 0; x < 32; ++x)
-                s[x] = __float_as_uint(fmaf(-slope, fabsf(far - (float)x), __uint_as_float(s[x])));
+              for (int y = 0; y < 32; ++y)
+                s[y] = __float_as_uint(fmaf(-slope, fabsf(far - (float)y), __uint_as_float(s[y])));
             }
+            if (!whole) {
 #pragma unroll
-            for (int x = 0; x < 32; ++x) {
-              const float v = (bits >> x) & 1u ? __uint_as_float(s[x]) : -INFINITY;
-              top = fmaxf(top, v);
-              s[x] = __float_as_uint(v);
+              for (int y = 0; y < 32; ++y)
+                if (!((bits >> y) & 1u)) s[y] = __float_as_uint(-INFINITY);
             }
+            top = fmaxf(top, max32(s));
             tc_st32(tS + 32 * c, s);
           }
           tc_wait_st();
+          tc_ld32(tS, sa);
+          top *= c1;
+          if (__any_sync(kFull, top > ref + kDtAhead)) rebase(fmaxf(ref, top));
         }
-        const float mn = fmaxf(mx, top * c1);
-        const float base = mn == -INFINITY ? 0.f : mn;  // nothing seen yet: scores are -inf or NaN, weights 0 or NaN
-        const float prev = corr;
-        corr = mn == -INFINITY ? 1.f : ex2(mx - mn);
-        mx = mn;
-        const uint64_t nb = pack2(-base, -base), minus = pack2(-1.f, -1.f);
-        uint64_t sum = 0;  // (0, 0)
-        uint32_t s[2][32];
-        tc_ld32(tS, s[0]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tc_wait_ld();
-          if (c < 3) tc_ld32(tS + 32 * (c + 1), s[(c + 1) & 1]);
+        // weights, 32 columns at a time, in place
+        const uint64_t minus = pack2(-1.f, -1.f);
+        float base = ref == -INFINITY ? 0.f : ref;  // nothing seen yet: scores are -inf or NaN, weights 0 or NaN
+        uint64_t total = 0;  // (0, 0)
+        auto weights = [&](int c, uint32_t (&s)[32]) {
           uint32_t w[32];  // 16 words of hi pairs, 16 of lo pairs
+          uint64_t sum0 = 0, sum1 = 0;
+          const uint64_t nb = pack2(-base, -base);
 #pragma unroll
-          for (int x = 0; x < 16; ++x) {
+          for (int y = 0; y < 16; ++y) {
             float a, e;
-            unpack2(fma2(pack2(__uint_as_float(s[c & 1][2 * x]), __uint_as_float(s[c & 1][2 * x + 1])), c2, nb), a, e);
+            unpack2(fma2(pack2(__uint_as_float(s[2 * y]), __uint_as_float(s[2 * y + 1])), c2, nb), a, e);
             a = ex2(a);
             e = ex2(e);
             const uint64_t w2 = pack2(a, e);
-            sum = add2(sum, w2);
+            if (y & 1) sum1 = add2(sum1, w2); else sum0 = add2(sum0, w2);
             const __nv_bfloat162 hi = __floats2bfloat162_rn(a, e);
-            w[x] = *reinterpret_cast<const uint32_t*>(&hi);
-            unpack2(fma2(pack2(bf16lo(w[x]), bf16hi(w[x])), minus, w2), a, e);
+            w[y] = *reinterpret_cast<const uint32_t*>(&hi);
+            unpack2(fma2(pack2(bf16lo(w[y]), bf16hi(w[y])), minus, w2), a, e);
             const __nv_bfloat162 low = __floats2bfloat162_rn(a, e);
-            w[16 + x] = *reinterpret_cast<const uint32_t*>(&low);
+            w[16 + y] = *reinterpret_cast<const uint32_t*>(&low);
           }
+          sum0 = add2(sum0, sum1);
+          float a, e;
+          unpack2(sum0, a, e);
+          if (__any_sync(kFull, a + e > kDtMost)) return false;
+          total = add2(total, sum0);
           tc_st32(tS + 32 * c, w);
+          return true;
+        };
+        // some weight of columns 32 c on is too large: a new reference from their scores, to which the
+        // weights of the columns before are brought
+        auto raise = [&](int c) {
+          uint32_t s[32];
+          tc_ld32(tS + 32 * c, s);
+          tc_wait_ld();
+          const float f = rebase(fmaxf(ref, max32(s) * c1));
+          base = ref;
+          total = mul2(total, pack2(f, f));
+          tc_wait_st();
+#pragma unroll 1
+          for (int y = 0; y < 2 * c; ++y) {
+            uint32_t w[16];
+            tc_ld16u(tS + 32 * (y >> 1) + 8 * (y & 1), w);
+            tc_wait_ld();
+#pragma unroll
+            for (int z = 0; z < 8; ++z)
+              split2((bf16lo(w[z]) + bf16lo(w[8 + z])) * f, (bf16hi(w[z]) + bf16hi(w[8 + z])) * f, w[z], w[8 + z]);
+            tc_st16u(tS + 32 * (y >> 1) + 8 * (y & 1), w);
+          }
+          tc_wait_st();
+        };
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          tc_wait_ld();
+          if (!weights(c, sa)) {
+            raise(c);
+            tc_ld32(tS + 32 * c, sa);
+            tc_wait_ld();
+            weights(c, sa);  // the largest is 1 now (or NaN)
+          }
+          if (c < 3) tc_ld32(tS + 32 * (c + 1), sa);
         }
         float sum0, sum1;
-        unpack2(sum, sum0, sum1);
-        l = fmaf(l, corr, sum0 + sum1);
+        unpack2(total, sum0, sum1);
+        l += sum0 + sum1;
         tc_wait_st();
-        tc_fence_before();
-        mbar_arrive(&pfull[m]);
-        // off the way of the tensor cores where there are two O: the one before this tile's
-        if (kTwoO && j > 0) add_o(tO + (uint32_t)((j - 1) & 1) * 64, prev);
-      } else {
-        tc_fence_before();
-        mbar_arrive(&pfull[m]);
       }
+      // every kDtDrain tiles O goes to acc, and this tile's product starts it anew
+      if (j > 0 && j % kDtDrain == 0) {
+        if (!o_there(j - 1)) ok = false;
+        if (work && ok) add_o();
+      }
+      if (!__all_sync(kFull, ok)) {
+        ok = false;
+        break;
+      }
+      tc_fence_before();
+      mbar_arrive(&pfull[x % NB]);
     }
     if (n > 0 && ok) {
       if (!__all_sync(kFull, mbar_wait_bounded(odone, 0))) ok = false;
       tc_fence_after();
-      if (ok && work && mine > 0) add_o(tO + (kTwoO ? (uint32_t)((mine - 1) & 1) * 64 : 0u), corr);
+      if (ok && work && mine > 0) add_o();
     }
+    float mx = ref;  // what l and acc are relative to
     if (!ok) l = __int_as_float(0x7fc00000);
     if (!two) {
       // the odd key tiles' result joins the even ones'; every product is done, so the K stages are free
@@ -570,59 +695,58 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         }
         ids = next;
       }
-    } else if (warp == 12 && lane == 0 && n > 0) {
+    } else if (warp == 12 && n > 0) {
       // ---------------------------------------------------------------- MMA
+      // items x = 0, 1, ...: warpgroup x & 1, its key tile; PV(x) frees x's buffer for S(x + NB)
+      const uint32_t leader = elect_leader();
       const uint32_t id_s = idesc_bf16(kDtM, kDtKeys);
       const uint32_t id_o = idesc_bf16(kDtM, r) | (1u << 16);  // B with its columns contiguous
       const uint64_t qdesc = smem_desc_sw128(sQ), kdesc = smem_desc_sw128(smem + lay.k), cdesc = dt_cdesc(smem + lay.c);
-      ok = mbar_wait_bounded(qfull, 0);
-      const int steps = two ? n : (n + 1) / 2;
-      for (int j = 0; j <= steps && ok; ++j) {
-#pragma unroll 1
-        for (int m = 0; m < 2; ++m) {
-          const int tp = two ? j - 1 : 2 * (j - 1) + m, tc = two ? j : 2 * j + m;  // key tiles of PV, of S
-          const bool first = !two || m == 0, last = !two || m == 1;  // the tile's first and last use
-          if (j > 0 && tp < n) {
-            const int s = tp % CS;
-            if ((first && !mbar_wait_bounded(&cfull[s], (uint32_t)((tp / CS) & 1))) ||
-                !mbar_wait_bounded(&pfull[m], (uint32_t)((j - 1) & 1))) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint64_t bd = cdesc + (uint64_t)((uint32_t)s * c_stage >> 4);
-            const uint32_t o = tmem + 256 + (uint32_t)m * 128 + (kTwoO ? (uint32_t)((j - 1) & 1) * 64 : 0u);
-            const uint32_t pa = tmem + (uint32_t)m * 128;
-#pragma unroll
-            for (int x = 0; x < kDtKeys / 16; ++x) {
-              const uint32_t at = pa + (x >> 1) * 32 + (x & 1) * 8;
-              dt_mma_ts(o, at, bd + x * 128, id_o, x > 0);
-              dt_mma_ts(o, at + 16, bd + x * 128, id_o, true);
-            }
-            if (last) tc_commit(&cempty[s]);
+      const int items = two ? 2 * n : n;
+      ok = __all_sync(kFull, mbar_wait_bounded(qfull, 0));
+      for (int x = -NB; x < items && ok; ++x) {
+        if (x >= 0) {
+          const int j = two ? x >> 1 : x, s = j % CS, m = x & 1, buf = x % NB;
+          if (!__all_sync(kFull, mbar_wait_bounded(&cfull[s], (uint32_t)((j / CS) & 1)) &&
+                                     mbar_wait_bounded(&pfull[buf], (uint32_t)((x / NB) & 1)))) {
+            ok = false;
+            break;
           }
-          if (tc < n) {
-            const int s = tc % kDtK;
-            if (first && !mbar_wait_bounded(&kfull[s], (uint32_t)((tc / kDtK) & 1))) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint64_t ad = qdesc + (uint64_t)(two ? ((uint32_t)m * k_stage >> 4) : 0u);
-            const uint64_t bd = kdesc + (uint64_t)((uint32_t)s * k_stage >> 4);
+          tc_fence_after();
+          const uint64_t bd = cdesc + (uint64_t)((uint32_t)s * c_stage >> 4);
+          const bool join = (x >> 1) % kDtDrain != 0;  // onto the O of the tiles before
+          const uint32_t o = tmem + tO0 + (uint32_t)m * tOstep, pa = tmem + (uint32_t)buf * 128;
 #pragma unroll
-            for (int x = 0; x < D / 16; ++x) {
-              const uint64_t step = (uint64_t)(((x >> 2) * kDtAtom + (x & 3) * 32) >> 4);
-              dt_mma_ss(tmem + (uint32_t)m * 128, ad + step, bd + step, id_s, x > 0);
-            }
-            tc_commit(&sfull[m]);
-            if (last) tc_commit(&kempty[s]);
+          for (int y = 0; y < kDtKeys / 16; ++y) {
+            const uint32_t at = pa + (y >> 1) * 32 + (y & 1) * 8;
+            dt_mma_ts(leader, o, at, bd + y * 128, id_o, y > 0 || join);
+            dt_mma_ts(leader, o, at + 16, bd + y * 128, id_o, true);
           }
+          dt_commit(leader, &ofull[m]);
+          if (!two || m == 1) dt_commit(leader, &cempty[s]);
+        }
+        const int z = x + NB;
+        if (z < items) {
+          const int j = two ? z >> 1 : z, s = j % kDtK, m = z & 1, buf = z % NB;
+          if (!__all_sync(kFull, mbar_wait_bounded(&kfull[s], (uint32_t)((j / kDtK) & 1)))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t ad = qdesc + (uint64_t)(two ? ((uint32_t)m * k_stage >> 4) : 0u);
+          const uint64_t bd = kdesc + (uint64_t)((uint32_t)s * k_stage >> 4);
+#pragma unroll
+          for (int y = 0; y < D / 16; ++y) {
+            const uint64_t step = (uint64_t)(((y >> 2) * kDtAtom + (y & 3) * 32) >> 4);
+            dt_mma_ss(leader, tmem + (uint32_t)buf * 128, ad + step, bd + step, id_s, y > 0);
+          }
+          dt_commit(leader, &sfull[buf]);
+          if (!two || m == 1) dt_commit(leader, &kempty[s]);
         }
       }
       // every product, or after a failed wait what was issued
-      tc_commit(odone);
-      if (!mbar_wait_bounded(odone, 0)) ok = false;
+      dt_commit(leader, odone);
+      if (!__all_sync(kFull, mbar_wait_bounded(odone, 0))) ok = false;
     }
   }
   if (!ok) set_err(p.err, BASISKV_DEVERR_TIMEOUT);
@@ -688,24 +812,30 @@ static cudaError_t page_map(CUtensorMap* map, const void* base, int cols, int pa
   return e == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int D, int RMAX>
+template <int D, int RMAX, bool MOD>
 static cudaError_t launch_dt(const DenseParams& p, cudaStream_t st) {
   constexpr size_t smem = dt_layout<D, RMAX>().total + 1024;
   static_assert(smem <= 227 * 1024, "shared memory of a CTA");
-  cudaError_t e = ensure_smem((const void*)dense_tc_kernel<D, RMAX>, smem);
+  cudaError_t e = ensure_smem((const void*)dense_tc_kernel<D, RMAX, MOD>, smem);
   if (e != cudaSuccess) return e;
   CUtensorMap kmap{}, cmap{};
   const long long blocks = (long long)p.num_phys * p.Hkv;
   if ((e = page_map(&kmap, p.k_raw, D, p.page, blocks)) != cudaSuccess) return e;
   if (p.r % 64 == 0 && (e = page_map(&cmap, p.c_lat, p.r, p.page, blocks)) != cudaSuccess) return e;
   const long long units = ((long long)p.n_new * p.G + kDtRows - 1) / kDtRows * p.Hkv * p.batch;
-  dense_tc_kernel<D, RMAX><<<(unsigned)(units * p.splits), kDtThreads, smem, st>>>(p, kmap, cmap);
+  dense_tc_kernel<D, RMAX, MOD><<<(unsigned)(units * p.splits), kDtThreads, smem, st>>>(p, kmap, cmap);
   return cudaGetLastError();
 }
 
+template <bool MOD>
+static cudaError_t launch_dt_shape(const DenseParams& p, cudaStream_t st) {
+  if (p.d == 64) return launch_dt<64, 64, MOD>(p, st);
+  return p.r <= 64 ? launch_dt<128, 64, MOD>(p, st)
+       : p.r <= 96 ? launch_dt<128, 96, MOD>(p, st) : launch_dt<128, 128, MOD>(p, st);
+}
+
 cudaError_t launch_dense_tc(const DenseParams& p, cudaStream_t st) {
-  if (p.d == 64) return launch_dt<64, 64>(p, st);
-  return p.r <= 64 ? launch_dt<128, 64>(p, st) : p.r <= 96 ? launch_dt<128, 96>(p, st) : launch_dt<128, 128>(p, st);
+  return p.cap > 0.f || p.slopes ? launch_dt_shape<true>(p, st) : launch_dt_shape<false>(p, st);
 }
 
 }  // namespace bkv
