@@ -203,6 +203,24 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
   lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 
+// Barrier operations of a whole warp.  It waits together, the verdict a vote, so that it stays converged; and one
+// lane arrives for it (32 arrivals at one barrier take their turns in shared memory).
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
+  const long long t0 = clock64();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
+    if (__any_sync(kFull, clock64() - t0 > 2000000000LL)) return false;  // about a second
+  }
+}
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+  __syncwarp();
+}
+
 // barrier of the 96 threads of warps 9-11: whether `x` holds in all of them
 __device__ __forceinline__ bool all_of_96(bool x) {
   uint32_t y;
@@ -278,10 +296,10 @@ __global__ void __launch_bounds__(kDtThreads, 1)
       mbar_init(&cfull[s], 1);
       mbar_init(&cempty[s], 1);
     }
-    mbar_init(qfull, two ? 256 : 128);
+    mbar_init(qfull, two ? 8 : 4);
     for (int x = 0; x < NB; ++x) {
       mbar_init(&sfull[x], 1);
-      mbar_init(&pfull[x], 128);
+      mbar_init(&pfull[x], 4);
     }
     mbar_init(&ofull[0], 1);
     mbar_init(&ofull[1], 1);
@@ -318,7 +336,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
       cp_async_commit_group();
       cp_async_wait_group<0>();
       fence_proxy_async_smem();
-      mbar_arrive(qfull);
+      warp_arrive(qfull, lane);
     }
     const bool work = (row & ~31) < rows;  // this warp holds rows
     // first and last position of the warpgroup's rows
@@ -354,7 +372,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
       }
     };
     auto o_there = [&](int j) {  // the product of this warpgroup's tile j is in O
-      const bool there = __all_sync(kFull, mbar_wait_bounded(&ofull[m], (uint32_t)(j & 1)));
+      const bool there = warp_wait(&ofull[m], (uint32_t)(j & 1));
       tc_fence_after();
       return there;
     };
@@ -362,7 +380,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
     for (int j = 0; j < mine; ++j) {
       const int x = 2 * j + m;  // the item: S buffer x % NB, for the x / NB th time
       const uint32_t tS = tw + (uint32_t)(x % NB) * 128;
-      if (!__all_sync(kFull, mbar_wait_bounded(&sfull[x % NB], (uint32_t)((x / NB) & 1)))) {
+      if (!warp_wait(&sfull[x % NB], (uint32_t)((x / NB) & 1))) {
         ok = false;
         break;
       }
@@ -533,10 +551,10 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         break;
       }
       tc_fence_before();
-      mbar_arrive(&pfull[x % NB]);
+      warp_arrive(&pfull[x % NB], lane);
     }
     if (n > 0 && ok) {
-      if (!__all_sync(kFull, mbar_wait_bounded(odone, 0))) ok = false;
+      if (!warp_wait(odone, 0)) ok = false;
       tc_fence_after();
       if (ok && work && mine > 0) add_o();
     }
@@ -583,6 +601,9 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         if (p.lse) p.lse[at] = l > 0.f ? (mx + log2f(l)) * kLn2 : (l == l ? -INFINITY : l);
       }
     }
+    // what follows is common code, for which every warp has the registers it was compiled with
+    __syncwarp();
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(128));
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(256 - dt_regs<RMAX>()));
     // physical page of lane x < np of key tile j: -1 where no row sees any of it, or for a bad entry
@@ -610,7 +631,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         const uint32_t bits = __ballot_sync(kFull, ids >= 0);
         if (j < n) {
           const int s = j % kDtK;
-          if (j >= kDtK && !__all_sync(kFull, mbar_wait_bounded(&kempty[s], (uint32_t)((j / kDtK - 1) & 1)))) {
+          if (j >= kDtK && !warp_wait(&kempty[s], (uint32_t)((j / kDtK - 1) & 1))) {
             ok = false;
             break;
           }
@@ -629,7 +650,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         }
         // (each role waits for every tile's stage, its own or not: a parity says nothing two phases on)
         if (j - 1 >= CS &&
-            !__all_sync(kFull, mbar_wait_bounded(&cempty[(j - 1) % CS], (uint32_t)(((j - 1) / CS - 1) & 1)))) {
+            !warp_wait(&cempty[(j - 1) % CS], (uint32_t)(((j - 1) / CS - 1) & 1))) {
           ok = false;
           break;
         }
@@ -648,10 +669,10 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         ids = next;
       }
       // no copy is on its way when the CTA ends, whatever became of the other warps
-      for (int j = max(0, issued - kDtK); j < issued; ++j) mbar_wait_bounded(&kfull[j % kDtK], (uint32_t)((j / kDtK) & 1));
+      for (int j = max(0, issued - kDtK); j < issued; ++j) warp_wait(&kfull[j % kDtK], (uint32_t)((j / kDtK) & 1));
       // (a C stage that a later tile took was read, so its copy had landed)
       for (int j = max(0, (ok ? n : last_c + 1) - CS); j <= last_c; ++j)
-        mbar_wait_bounded(&cfull[j % CS], (uint32_t)((j / CS) & 1));
+        warp_wait(&cfull[j % CS], (uint32_t)((j / CS) & 1));
     } else if (warp < 12) {
       // ---------------------------------------------------------------- the other C tiles, by 96 threads
       const int ct = tid - 288, cc = r / 8;
@@ -663,7 +684,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         const uint32_t bits = __ballot_sync(kFull, ids >= 0);
         const int s = j % CS;
         if (j >= CS) {
-          ok = all_of_96(mbar_wait_bounded(&cempty[s], (uint32_t)((j / CS - 1) & 1)));  // the three warps give up together
+          ok = all_of_96(warp_wait(&cempty[s], (uint32_t)((j / CS - 1) & 1)));  // the three warps give up together
           if (!ok) break;
         }
         if (!c_by_tma(j, bits)) {
@@ -703,12 +724,12 @@ __global__ void __launch_bounds__(kDtThreads, 1)
       const uint32_t id_o = idesc_bf16(kDtM, r) | (1u << 16);  // B with its columns contiguous
       const uint64_t qdesc = smem_desc_sw128(sQ), kdesc = smem_desc_sw128(smem + lay.k), cdesc = dt_cdesc(smem + lay.c);
       const int items = two ? 2 * n : n;
-      ok = __all_sync(kFull, mbar_wait_bounded(qfull, 0));
+      ok = warp_wait(qfull, 0);
       for (int x = -NB; x < items && ok; ++x) {
         if (x >= 0) {
           const int j = two ? x >> 1 : x, s = j % CS, m = x & 1, buf = x % NB;
-          if (!__all_sync(kFull, mbar_wait_bounded(&cfull[s], (uint32_t)((j / CS) & 1)) &&
-                                     mbar_wait_bounded(&pfull[buf], (uint32_t)((x / NB) & 1)))) {
+          if (!warp_wait(&cfull[s], (uint32_t)((j / CS) & 1)) ||
+              !warp_wait(&pfull[buf], (uint32_t)((x / NB) & 1))) {
             ok = false;
             break;
           }
@@ -728,7 +749,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         const int z = x + NB;
         if (z < items) {
           const int j = two ? z >> 1 : z, s = j % kDtK, m = z & 1, buf = z % NB;
-          if (!__all_sync(kFull, mbar_wait_bounded(&kfull[s], (uint32_t)((j / kDtK) & 1)))) {
+          if (!warp_wait(&kfull[s], (uint32_t)((j / kDtK) & 1))) {
             ok = false;
             break;
           }
@@ -746,8 +767,10 @@ __global__ void __launch_bounds__(kDtThreads, 1)
       }
       // every product, or after a failed wait what was issued
       dt_commit(leader, odone);
-      if (!__all_sync(kFull, mbar_wait_bounded(odone, 0))) ok = false;
+      if (!warp_wait(odone, 0)) ok = false;
     }
+    __syncwarp();
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(128));
   }
   if (!ok) set_err(p.err, BASISKV_DEVERR_TIMEOUT);
   tc_fence_before();
