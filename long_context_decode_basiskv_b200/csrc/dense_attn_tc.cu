@@ -283,6 +283,9 @@ __global__ void __launch_bounds__(kDtThreads, 1)
   if (sq.L > 0) kt = key_tiles(pos0 + t_lo, pos0 + t_hi, sq.L, p.window, sq.prefix, kDtKeys);
   const int lo = (int)((long long)kt.count() * split / p.splits);
   const int n = (int)((long long)kt.count() * (split + 1) / p.splits) - lo;  // key tiles of this CTA
+  // Key tiles are taken from the last to the first: the first one then has the rows' own positions, where a
+  // distance bias leaves the scores highest, and its maximum serves as reference for the others.
+  auto tile_at = [&](int j) { return kt.tile(lo + n - 1 - j); };
   // keys that some row of the CTA sees: [0, prefix) and [see_lo, see_hi)
   const int see_lo = p.window > 0 ? pos0 + t_lo - p.window + 1 : 0;
   const int see_hi = min(sq.L, max(pos0 + t_hi + 1, sq.prefix));
@@ -389,10 +392,45 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         uint32_t sa[32];
         tc_ld32(tS, sa);
         const int jt = two ? j : x;
-        const int j0 = kt.tile(lo + jt) * kDtKeys;
+        const int j0 = tile_at(jt) * kDtKeys;
         const uint32_t pages = s_pages[jt % kDtMasks];
         const bool whole = pages == (1u << np) - 1u &&
             (j0 + kDtKeys <= sq.prefix || (j0 + kDtKeys - 1 <= i0 && (p.window == 0 || i1 - j0 < p.window)));
+        // raw scores of columns 32 c on -> capped and biased, in units of log 2
+        auto modify = [&](int c, uint32_t (&s)[32]) {
+          if (p.cap > 0.f) {
+            float big = 0.f;
+#pragma unroll
+            for (int y = 0; y < 32; ++y) big = fmaxf(big, fabsf(__uint_as_float(s[y])));
+            const uint64_t sc2 = pack2(p.scale, p.scale), cap2 = pack2(p.cap, p.cap);
+            if (__any_sync(kFull, !(big * p.scale <= 1.f))) {
+#pragma unroll
+              for (int y = 0; y < 32; ++y) s[y] = __float_as_uint(cap_score(__uint_as_float(s[y]) * p.scale, p.cap));
+            } else {
+#pragma unroll
+              for (int y = 0; y < 32; y += 2) {
+                const uint64_t v = mul2(pack2(__uint_as_float(s[y]), __uint_as_float(s[y + 1])), sc2);
+                const uint64_t v2 = mul2(v, v);
+                uint64_t t2 = pack2(tanh_coef(kTanhTop), tanh_coef(kTanhTop));
+#pragma unroll
+                for (int k = kTanhTop - 1; k >= 0; --k) t2 = fma2(t2, v2, pack2(tanh_coef(k), tanh_coef(k)));
+                float y0, y1;
+                unpack2(mul2(mul2(t2, v), cap2), y0, y1);
+                s[y] = __float_as_uint(y0);
+                s[y + 1] = __float_as_uint(y1);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int y = 0; y < 32; ++y) s[y] = __float_as_uint(__uint_as_float(s[y]) * p.scale);
+          }
+          if (p.slopes) {
+            const float far = (float)(pos - j0 - 32 * c);
+#pragma unroll
+            for (int y = 0; y < 32; ++y)
+              s[y] = __float_as_uint(fmaf(-slope, fabsf(far - (float)y), __uint_as_float(s[y])));
+          }
+        };
         // A new reference: f takes what was summed relative to the old one to it.  O of the tiles since the
         // last one that went to acc is rescaled where it is.
         auto rebase = [&](float nref) {
@@ -415,7 +453,8 @@ __global__ void __launch_bounds__(kDtThreads, 1)
           }
           return f;
         };
-        if (MOD || !whole || __any_sync(kFull, ref == -INFINITY)) {
+        const bool first_pass = !whole || __any_sync(kFull, ref == -INFINITY);
+        if (first_pass) {
           // scores as they count, written back over S, and their maximum.  Seen keys of the tile, as bits:
           // the range that the row's position and window give, and the prefix
           float top = -INFINITY;
@@ -428,38 +467,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
             if (P == 16) bits &= ((pages >> (2 * c) & 1u) ? 0x0000ffffu : 0u) | ((pages >> (2 * c + 1) & 1u) ? 0xffff0000u : 0u);
             else if (!((pages >> ((32 * c) >> psh)) & 1u)) bits = 0;
             tc_wait_ld();
-            if (MOD && p.cap > 0.f) {
-              float big = 0.f;
-#pragma unroll
-              for (int y = 0; y < 32; ++y) big = fmaxf(big, fabsf(__uint_as_float(s[y])));
-              const uint64_t sc2 = pack2(p.scale, p.scale), cap2 = pack2(p.cap, p.cap);
-              if (__any_sync(kFull, !(big * p.scale <= 1.f))) {
-#pragma unroll
-                for (int y = 0; y < 32; ++y) s[y] = __float_as_uint(cap_score(__uint_as_float(s[y]) * p.scale, p.cap));
-              } else {
-#pragma unroll
-                for (int y = 0; y < 32; y += 2) {
-                  const uint64_t v = mul2(pack2(__uint_as_float(s[y]), __uint_as_float(s[y + 1])), sc2);
-                  const uint64_t v2 = mul2(v, v);
-                  uint64_t t2 = pack2(tanh_coef(kTanhTop), tanh_coef(kTanhTop));
-#pragma unroll
-                  for (int k = kTanhTop - 1; k >= 0; --k) t2 = fma2(t2, v2, pack2(tanh_coef(k), tanh_coef(k)));
-                  float y0, y1;
-                  unpack2(mul2(mul2(t2, v), cap2), y0, y1);
-                  s[y] = __float_as_uint(y0);
-                  s[y + 1] = __float_as_uint(y1);
-                }
-              }
-            } else if (MOD) {
-#pragma unroll
-              for (int y = 0; y < 32; ++y) s[y] = __float_as_uint(__uint_as_float(s[y]) * p.scale);
-            }
-            if (MOD && p.slopes) {
-              const float far = (float)(pos - j0 - 32 * c);
-#pragma unroll
-              for (int y = 0; y < 32; ++y)
-                s[y] = __float_as_uint(fmaf(-slope, fabsf(far - (float)y), __uint_as_float(s[y])));
-            }
+            if (MOD) modify(c, s);
             if (!whole) {
 #pragma unroll
               for (int y = 0; y < 32; ++y)
@@ -478,6 +486,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         float base = ref == -INFINITY ? 0.f : ref;  // nothing seen yet: scores are -inf or NaN, weights 0 or NaN
         uint64_t total = 0;  // (0, 0)
         auto weights = [&](int c, uint32_t (&s)[32]) {
+          if (MOD && !first_pass) modify(c, s);
           uint32_t w[32];  // 16 words of hi pairs, 16 of lo pairs
           uint64_t sum0 = 0, sum1 = 0;
           const uint64_t nb = pack2(-base, -base);
@@ -509,6 +518,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
           uint32_t s[32];
           tc_ld32(tS + 32 * c, s);
           tc_wait_ld();
+          if (MOD && !first_pass) modify(c, s);
           const float f = rebase(fmaxf(ref, max32(s) * c1));
           base = ref;
           total = mul2(total, pack2(f, f));
@@ -610,14 +620,14 @@ __global__ void __launch_bounds__(kDtThreads, 1)
     auto pages_of = [&](int j) {
       int id = -1;
       if (j < n && lane < np) {
-        const int first = kt.tile(lo + j) * kDtKeys + (lane << psh);
+        const int first = tile_at(j) * kDtKeys + (lane << psh);
         if (first < see_hi && (first + P > see_lo || first < sq.prefix)) id = dense_page(p, b, first >> psh);
       }
       return id;
     };
     // C tile j comes by TMA: whole swizzle atoms, every token seen by some row
     auto c_by_tma = [&](int j, uint32_t bits) {
-      const int j0 = kt.tile(lo + j) * kDtKeys;
+      const int j0 = tile_at(j) * kDtKeys;
       return r % 64 == 0 && bits == (1u << np) - 1u && j0 + kDtKeys <= see_hi &&
              (j0 >= see_lo || j0 + kDtKeys <= sq.prefix);
     };
@@ -688,7 +698,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
           if (!ok) break;
         }
         if (!c_by_tma(j, bits)) {
-          const int j0 = kt.tile(lo + j) * kDtKeys;
+          const int j0 = tile_at(j) * kDtKeys;
           unsigned char* dst = smem + lay.c + (size_t)s * c_stage;
           int row = ct / cc, ch = ct - row * cc;
 #pragma unroll 4
