@@ -329,7 +329,7 @@ static basiskv_status pages_common(const basiskv_config* cfg, int32_t batch, int
     return BASISKV_ERR_INVALID_ARG;
   *p = PagesParams{seq_len, amount, const_cast<int32_t*>(table), const_cast<int32_t*>(free_pages), free_count,
                    seq_len_out, free_count_out, slots, err_flag, batch, cfg->page_size, max_pages, num_phys,
-                   slot_cols, (slot_cols % 4 == 0 && aligned16(slots)) ? 4 : 1};
+                   slot_cols, (slot_cols % 4 == 0 && aligned16(slots)) ? 4 : 1, false};
   return BASISKV_OK;
 }
 

@@ -152,6 +152,7 @@ struct PagesParams {
   int32_t* slots;  // [B][slot_cols] or NULL
   int32_t* err;
   int batch, page, max_pages, num_phys, slot_cols, slot_vec;
+  bool rows_later;  // slots past the first of each request are another kernel's
 };
 cudaError_t launch_assign_pages(const PagesParams& p, cudaStream_t st);
 cudaError_t launch_release_pages(const PagesParams& p, cudaStream_t st);

@@ -21,7 +21,7 @@ constexpr int kPageThreads = 1024;
 // A cluster of 8 CTAs (the portable limit) for anything but the smallest
 // calls, whose few stores one CTA issues as fast without the cluster's start.
 constexpr int kPageCluster = 8;
-constexpr long long kPageSmall = 8192;  // slots, or requests, that one CTA serves
+constexpr long long kPageSmall = 8192;  // slots, or pages, that one CTA writes
 
 // the request that page p of the flattened new (or released) pages belongs to
 __device__ __forceinline__ int request_of(const int* off, int B, int p) {
@@ -79,6 +79,7 @@ __global__ void __launch_bounds__(kPageThreads) pages_kernel(PagesParams p) {
   // the page ids this call hands on, checked before anything is written
   const int gt = rank * kPageThreads + tid, nt = C * kPageThreads;
   if (!(bad & BASISKV_DEVERR_PAGES)) {  // the same for every thread of the cluster
+#pragma unroll 4
     for (int i = gt; i < total; i += nt) {
       int id;
       if (ASSIGN) {
@@ -102,10 +103,14 @@ __global__ void __launch_bounds__(kPageThreads) pages_kernel(PagesParams p) {
   __syncthreads();
   bad = s_bad;
   if (C > 1) {  // the others' bits; nobody leaves while its own may still be read
+    __shared__ uint32_t s_all;
+    if (tid == 0) s_all = 0;
     cluster_arrive_release();
     cluster_wait_acquire();
-    for (int c = 0; c < C; ++c) bad |= ld_shared_cluster(&s_bad, (uint32_t)c);
+    if (tid < C) atomicOr(&s_all, ld_shared_cluster(&s_bad, (uint32_t)tid));
     cluster_arrive_relaxed();
+    __syncthreads();
+    bad = s_all;
   }
 
   if (rank == 0) {
@@ -119,6 +124,7 @@ __global__ void __launch_bounds__(kPageThreads) pages_kernel(PagesParams p) {
     }
   }
   if (!bad) {
+#pragma unroll 4
     for (int i = gt; i < total; i += nt) {
       const int b = request_of(s_off, B, i);
       if (ASSIGN)
@@ -127,35 +133,25 @@ __global__ void __launch_bounds__(kPageThreads) pages_kernel(PagesParams p) {
         p.free_pages[count + i] = p.table[(size_t)b * p.max_pages + (i - s_off[b])];
     }
   }
+  // slots: all of them where they are few, else each request's first (-1 after a fault), from which
+  // slots_kernel goes on
   if (ASSIGN && p.slots) {
-    const int v = p.slot_vec, cols = p.slot_cols / v;  // v slots to a store
+    const int cols = p.rows_later ? 1 : p.slot_cols;
     const int db = nt / cols, dc = nt - db * cols;
-    int b = gt / cols, c = gt - b * cols;
+    int b = gt / cols, t = gt - b * cols;
     while (b < B) {
-      int w[4] = {-1, -1, -1, -1};
-      const int t0 = c * v, a = bad ? 0 : p.amount[b];
-      if (t0 < a) {
-        const int L = s_len[b], have = (L + P - 1) >> sh;
-        int page = -1, id = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (j < v && t0 + j < a) {
-            const int pos = L + t0 + j, pg = pos >> sh;
-            if (pg != page) {
-              page = pg;
-              id = pg < have ? p.table[(size_t)b * p.max_pages + pg] : p.free_pages[count - 1 - (s_off[b] + pg - have)];
-            }
-            w[j] = (id << sh) + (pos & (P - 1));
-          }
-        }
+      int w = -1;
+      if (!bad && t < p.amount[b]) {
+        const int L = s_len[b], have = (L + P - 1) >> sh, pos = L + t, pg = pos >> sh;
+        const int id = pg < have ? p.table[(size_t)b * p.max_pages + pg]
+                                 : p.free_pages[count - 1 - (s_off[b] + pg - have)];
+        w = (id << sh) + (pos & (P - 1));
       }
-      int* out = p.slots + (size_t)b * p.slot_cols + t0;
-      if (v == 4) *reinterpret_cast<int4*>(out) = make_int4(w[0], w[1], w[2], w[3]);
-      else *out = w[0];
+      p.slots[(size_t)b * p.slot_cols + t] = w;
       b += db;
-      c += dc;
-      if (c >= cols) {
-        c -= cols;
+      t += dc;
+      if (t >= cols) {
+        t -= cols;
         ++b;
       }
     }
@@ -163,13 +159,48 @@ __global__ void __launch_bounds__(kPageThreads) pages_kernel(PagesParams p) {
   if (C > 1) cluster_wait_acquire();
 }
 
+// The slots of many tokens, over the whole GPU: the kernel before it has set the table, the lengths and
+// each request's first slot, which says whether the call was met.
+constexpr int kSlotThreads = 256;
+__global__ void __launch_bounds__(kSlotThreads) slots_kernel(PagesParams p) {
+  grid_dep_wait();
+  const int b = blockIdx.y, P = p.page, sh = 31 - __clz(P);
+  const int t0 = (blockIdx.x * kSlotThreads + threadIdx.x) * 4;
+  if (t0 >= p.slot_cols) return;
+  int* row = p.slots + (size_t)b * p.slot_cols;
+  const int a = __ldcg(row) < 0 ? 0 : p.amount[b], pos = p.seq_len_out[b] - a + t0;
+  const int32_t* table = p.table + (size_t)b * p.max_pages;
+  const int left = min(4, a - t0);
+  int id0 = 0, id1 = 0;
+  if (left > 0) {
+    id0 = table[pos >> sh];
+    id1 = table[(pos + left - 1) >> sh];  // four tokens lie on two pages at most
+  }
+  int w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int at = pos + j;
+    w[j] = j < left ? (((at >> sh) == (pos >> sh) ? id0 : id1) << sh) + (at & (P - 1)) : -1;
+  }
+  if (p.slot_vec == 4) {
+    *reinterpret_cast<int4*>(row + t0) = make_int4(w[0], w[1], w[2], w[3]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (t0 + j < p.slot_cols) row[t0 + j] = w[j];
+  }
+}
+
 template <bool ASSIGN>
-static cudaError_t launch_pages_t(const PagesParams& p, cudaStream_t st) {
+static cudaError_t launch_pages_t(PagesParams p, cudaStream_t st) {
   const size_t smem = ((size_t)2 * p.batch + 1) * sizeof(int);
   cudaError_t e = ensure_smem((const void*)pages_kernel<ASSIGN>, smem);
   if (e != cudaSuccess) return e;
-  const long long slots = (ASSIGN && p.slots) ? (long long)p.batch * p.slot_cols : (long long)p.batch * 128;
-  const int C = slots <= kPageSmall ? 1 : kPageCluster;
+  // what the call may have to write: slots, or pages
+  const bool with_slots = ASSIGN && p.slots;
+  const long long most = (long long)p.batch * (with_slots ? p.slot_cols : p.max_pages);
+  const int C = most <= kPageSmall ? 1 : kPageCluster;
+  p.rows_later = with_slots && most > kPageSmall;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(C);
   cfg.blockDim = dim3(kPageThreads);
@@ -182,7 +213,13 @@ static cudaError_t launch_pages_t(const PagesParams& p, cudaStream_t st) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, pages_kernel<ASSIGN>, p);
+  if ((e = cudaLaunchKernelEx(&cfg, pages_kernel<ASSIGN>, p)) != cudaSuccess || !p.rows_later) return e;
+  cfg.gridDim = dim3((p.slot_cols + 4 * kSlotThreads - 1) / (4 * kSlotThreads), p.batch);
+  cfg.blockDim = dim3(kSlotThreads);
+  cfg.dynamicSmemBytes = 0;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  return cudaLaunchKernelEx(&cfg, slots_kernel, p);
 }
 
 cudaError_t launch_assign_pages(const PagesParams& p, cudaStream_t st) { return launch_pages_t<true>(p, st); }
