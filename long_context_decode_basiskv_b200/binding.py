@@ -144,9 +144,14 @@ class Config:
         return self.num_q_heads // self.num_kv_heads
 
     def c(self) -> CConfig:
-        return CConfig(self.num_q_heads, self.num_kv_heads, self.head_dim, self.rank_v, self.rank_k,
-                       self.page_size, self.hidden, self.top_k,
-                       BF16 if self.dtype == torch.bfloat16 else F32)
+        """The C struct (made once: no call writes to it)."""
+        made = self.__dict__.get("_c")
+        if made is None:
+            made = CConfig(self.num_q_heads, self.num_kv_heads, self.head_dim, self.rank_v, self.rank_k,
+                           self.page_size, self.hidden, self.top_k,
+                           BF16 if self.dtype == torch.bfloat16 else F32)
+            object.__setattr__(self, "_c", made)
+        return made
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -154,6 +159,9 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _need(t: torch.Tensor, name: str, dtype=None, shape=None):
+    if (type(t) is torch.Tensor and t.is_cuda and (dtype is None or t.dtype is dtype)
+            and (shape is None or t.shape == shape) and t.is_contiguous()):
+        return  # the common case, in one line: a decode step makes dozens of these checks
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -377,13 +385,14 @@ def decode_attn_noalloc(cfg: Config, cache: PagedCache, q: torch.Tensor, sel: to
                                              _stream(stream)), "basiskv_decode_attn_noalloc")
 
 
-def _same_device(first: torch.Tensor, **others):
+def _same_device(first: torch.Tensor, *others: Optional[torch.Tensor]):
     """Every tensor on `first`'s device, which must be the current one (the kernels launch there)."""
-    if first.device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {first.device}, the current device is cuda:{torch.cuda.current_device()}")
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} is on {t.device}, expected {first.device}")
+    d = first.get_device()
+    if d != torch.cuda.current_device():
+        raise ValueError(f"tensors are on cuda:{d}, the current device is cuda:{torch.cuda.current_device()}")
+    for t in others:
+        if t is not None and t.get_device() != d:
+            raise ValueError(f"a tensor is on {t.device}, the others are on cuda:{d}")
 
 
 def assign_pages(cfg: Config, block_table: torch.Tensor, seq_len: torch.Tensor, add_len: torch.Tensor,
@@ -407,8 +416,7 @@ def assign_pages(cfg: Config, block_table: torch.Tensor, seq_len: torch.Tensor, 
     _need(err, "err", i32)
     if slots is not None:
         _need(slots, "slots", i32, (B, slots.shape[1]) if slots.dim() == 2 else (B, -1))
-    _same_device(seq_len, block_table=block_table, add_len=add_len, free_pages=free_pages, free_count=free_count,
-                 seq_len_out=seq_len_out, free_count_out=free_count_out, slots=slots, err=err)
+    _same_device(seq_len, block_table, add_len, free_pages, free_count, seq_len_out, free_count_out, slots, err)
     _check(lib().basiskv_assign_pages(ctypes.byref(cfg.c()), B, max_pages, free_pages.numel(), _ptr(seq_len),
                                       _ptr(add_len), _ptr(block_table), _ptr(free_pages), _ptr(free_count),
                                       _ptr(seq_len_out), _ptr(free_count_out), _ptr(slots),
@@ -433,8 +441,7 @@ def release_pages(cfg: Config, block_table: torch.Tensor, seq_len: torch.Tensor,
     _need(seq_len_out, "seq_len_out", i32, (B,))
     _need(free_count_out, "free_count_out", i32, (1,))
     _need(err, "err", i32)
-    _same_device(seq_len, block_table=block_table, release=release, free_pages=free_pages, free_count=free_count,
-                 seq_len_out=seq_len_out, free_count_out=free_count_out, err=err)
+    _same_device(seq_len, block_table, release, free_pages, free_count, seq_len_out, free_count_out, err)
     _check(lib().basiskv_release_pages(ctypes.byref(cfg.c()), B, max_pages, free_pages.numel(), _ptr(seq_len),
                                        _ptr(release), _ptr(block_table), _ptr(free_pages), _ptr(free_count),
                                        _ptr(seq_len_out), _ptr(free_count_out), _ptr(err), _stream(stream)),
@@ -482,7 +489,7 @@ def _token_stride(t: torch.Tensor, name: str, dtype, shape) -> int:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     B, n, h, d = shape
     st = t.stride()
@@ -517,7 +524,7 @@ def rotary(cfg: Config, rope: Rope, q: Optional[torch.Tensor], k: Optional[torch
         _need(positions, "positions", torch.int32, (B, n))
     else:
         _need(seq_len, "seq_len", torch.int32, (B,))
-    _same_device(first, q=q, k=k, q_out=q_out, k_out=k_out, positions=positions, seq_len=seq_len)
+    _same_device(first, q, k, q_out, k_out, positions, seq_len)
     _check(lib().basiskv_rotary(ctypes.byref(cfg.c()), ctypes.byref(rope.c), _ptr(q), strides[0], _ptr(k), strides[1],
                                 _ptr(q_out), _ptr(k_out), _ptr(positions), _ptr(seq_len), B, n, _stream(stream)),
            "basiskv_rotary")
@@ -568,6 +575,6 @@ def dense_attn(cfg: Config, cache: PagedCache, q: torch.Tensor, o_lat: torch.Ten
         if prefix is not None:
             _need(prefix, "prefix_len", torch.int32, (B,))
         opt = ctypes.byref(CAttnOptions(options.scale, options.softcap, options.window, 0, _ptr(slopes), _ptr(prefix)))
-    _same_device(q, cache=cache.k_raw, o_lat=o_lat, workspace=ws, err=err, lse=lse, slopes=slopes, prefix_len=prefix)
+    _same_device(q, cache.k_raw, o_lat, ws, err, lse, slopes, prefix)
     _check(lib().basiskv_dense_attn(ctypes.byref(cfg.c()), ctypes.byref(cache.c()), _ptr(q), B, n, opt, _ptr(o_lat),
                                     _ptr(lse), _ptr(ws), ws.numel(), _ptr(err), _stream(stream)), "basiskv_dense_attn")
