@@ -10,9 +10,8 @@
 // ring of 1-D bulk copies (a tile of K and of C is contiguous in its page) and
 // works a tile on the tensor cores with the rows as the M of mma.sync m16n8k16
 // (tcgen05 has no shape below 64 rows): S = Q K^T, running maximum and sum,
-// O += P C.  The fp32 weights enter the second product as two bf16 terms, hi +
-// lo: 16 mantissa bits instead of 8, as out-projection and prefill do, for MMAs
-// that the stream hides.
+// O += P C.  The fp32 weights enter the second product as three bf16 terms (24
+// mantissa bits: o_lat is fp32), for MMAs that the stream hides.
 //
 // Where a run ends inside a sequence, the warp leaves (max, sum, acc) in its
 // slot: run w and group g meet in slot w + g, since along the tiles each step
@@ -57,12 +56,17 @@ __device__ __forceinline__ void dm_ldsm_t(uint32_t (&r)[4], uint32_t addr) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr));
 }
-// two fp32 values as a bf16 pair, and what it leaves of them as another
-__device__ __forceinline__ void dm_split(float a, float b, uint32_t& hi, uint32_t& lo) {
+__device__ __forceinline__ uint32_t dm_pack(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  hi = *reinterpret_cast<const uint32_t*>(&h);
-  const __nv_bfloat162 l = __floats2bfloat162_rn(a - bf16lo(hi), b - bf16hi(hi));
-  lo = *reinterpret_cast<const uint32_t*>(&l);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// two fp32 values as a bf16 pair, what it leaves of them as another, and what that leaves as a third: 24 bits
+__device__ __forceinline__ void dm_split(float a, float b, uint32_t& x, uint32_t& y, uint32_t& z) {
+  x = dm_pack(a, b);
+  a -= bf16lo(x);
+  b -= bf16hi(x);
+  y = dm_pack(a, b);
+  z = dm_pack(a - bf16lo(y), b - bf16hi(y));
 }
 
 // One sequence's rows and the tiles they see.
@@ -281,7 +285,7 @@ __global__ void __launch_bounds__(32 * kDmWarps, dm_ctas(D, NT * 8)) dense_mma_k
               dm_mma(sc[s2 & 1][1], qa[s2][0], a1, qa[s2][RB], a3, kb[2], kb[3]);
             }
           }
-          uint32_t ph[2][2], pl[2][2];  // [row block][8 tokens]
+          uint32_t pw[3][2][2];  // [term][row block][8 tokens]
           float corr[RB];
 #pragma unroll
           for (int y = 0; y < RB; ++y) {
@@ -309,17 +313,8 @@ __global__ void __launch_bounds__(32 * kDmWarps, dm_ctas(D, NT * 8)) dense_mma_k
             }
             m[y] = mn;
             l[y] = l[y] * corr[y] + ((pr[0] + pr[1]) + (pr[2] + pr[3]));
-            dm_split(pr[0], pr[1], ph[y][0], pl[y][0]);
-            dm_split(pr[2], pr[3], ph[y][1], pl[y][1]);
-          }
 #pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            acc[j][0] *= corr[0];
-            acc[j][1] *= corr[0];
-            if (ROWS16) {
-              acc[j][2] *= corr[RB - 1];
-              acc[j][3] *= corr[RB - 1];
-            }
+            for (int u = 0; u < 2; ++u) dm_split(pr[2 * u], pr[2 * u + 1], pw[0][y][u], pw[1][y][u], pw[2][y][u]);
           }
           {
             const int tok = (mi & 1) * 8 + rr;
@@ -328,12 +323,20 @@ __global__ void __launch_bounds__(32 * kDmWarps, dm_ctas(D, NT * 8)) dense_mma_k
             for (int jj = 0; jj < NT / 2; ++jj) {
               uint32_t cb[4];
               dm_ldsm_t(cb, rowaddr + (uint32_t)(((2 * jj + (mi >> 1)) ^ (tok & mc)) << 4));
-              const uint32_t h1 = ROWS16 ? ph[RB - 1][0] : 0u, h3 = ROWS16 ? ph[RB - 1][1] : 0u;
-              const uint32_t l1 = ROWS16 ? pl[RB - 1][0] : 0u, l3 = ROWS16 ? pl[RB - 1][1] : 0u;
-              dm_mma(acc[2 * jj], ph[0][0], h1, ph[0][1], h3, cb[0], cb[1]);
-              dm_mma(acc[2 * jj + 1], ph[0][0], h1, ph[0][1], h3, cb[2], cb[3]);
-              dm_mma(acc[2 * jj], pl[0][0], l1, pl[0][1], l3, cb[0], cb[1]);
-              dm_mma(acc[2 * jj + 1], pl[0][0], l1, pl[0][1], l3, cb[2], cb[3]);
+              // the tile's products on their own, then added in fp32: tensor cores cut off what they add
+              // up, which over a long run's tiles would cost more than the three terms keep
+              float t[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+              for (int z = 0; z < 3; ++z) {
+                const uint32_t a1 = ROWS16 ? pw[z][RB - 1][0] : 0u, a3 = ROWS16 ? pw[z][RB - 1][1] : 0u;
+                dm_mma(t[0], pw[z][0][0], a1, pw[z][0][1], a3, cb[0], cb[1]);
+                dm_mma(t[1], pw[z][0][0], a1, pw[z][0][1], a3, cb[2], cb[3]);
+              }
+#pragma unroll
+              for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int e = 0; e < 2 * RB; ++e)
+                  acc[2 * jj + u][e] = fmaf(acc[2 * jj + u][e], corr[e >> 1], t[u][e]);
             }
           }
         }
