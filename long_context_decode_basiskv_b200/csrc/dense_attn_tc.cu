@@ -43,7 +43,7 @@ constexpr int kDtKeys = 128;    // keys per tile
 constexpr int kDtThreads = 512; // 4 warpgroups: softmax, softmax, copies, MMA (one warp of it)
 constexpr int kDtK = 3;         // K stages
 constexpr int kDtMasks = 8;     // tiles whose page bits are kept: more than the copies run ahead
-constexpr int kDtDrain = 2;      // tiles whose products add up in tensor memory
+constexpr int kDtDrain = 4;      // tiles whose products add up in tensor memory
 constexpr float kDtAhead = 8.f;  // a reference is this far below a row's largest score at most, in a masked or modified
 constexpr float kDtMost = 65536.f; // tile; and the sum of 32 weights of a tile seen whole is at most this
 constexpr uint32_t kDtAtom = kDtKeys * 128;  // 128 rows x 128 bytes
