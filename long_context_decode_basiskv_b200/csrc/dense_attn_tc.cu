@@ -50,7 +50,7 @@ constexpr uint32_t kDtAtom = kDtKeys * 128;  // 128 rows x 128 bytes
 
 // C stages, and registers of a softmax thread: 512 x 128 at launch = 256 x softmax + 256 x (256 - softmax)
 template <int RMAX> constexpr int dt_cstages() { return RMAX <= 64 ? 3 : 2; }
-template <int RMAX> constexpr int dt_regs() { return RMAX <= 64 ? 192 : RMAX <= 96 ? 200 : 216; }
+template <int RMAX> constexpr int dt_regs() { return RMAX <= 64 ? 208 : RMAX <= 96 ? 216 : 224; }
 
 struct DtLayout {
   uint32_t q, k, c, bar, total;
@@ -399,26 +399,27 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         // raw scores of columns 32 c on -> capped and biased, in units of log 2
         auto modify = [&](int c, uint32_t (&s)[32]) {
           if (p.cap > 0.f) {
-            float big = 0.f;
-#pragma unroll
-            for (int y = 0; y < 32; ++y) big = fmaxf(big, fabsf(__uint_as_float(s[y])));
             const uint64_t sc2 = pack2(p.scale, p.scale), cap2 = pack2(p.cap, p.cap);
-            if (__any_sync(kFull, !(big * p.scale <= 1.f))) {
+            float far = 0.f;  // the largest x^2: beyond 1 the polynomial does not hold
+#pragma unroll
+            for (int y = 0; y < 32; y += 2) {
+              const uint64_t v = mul2(pack2(__uint_as_float(s[y]), __uint_as_float(s[y + 1])), sc2);
+              const uint64_t v2 = mul2(v, v);
+              uint64_t t2 = pack2(tanh_coef(kTanhTop), tanh_coef(kTanhTop));
+#pragma unroll
+              for (int k = kTanhTop - 1; k >= 0; --k) t2 = fma2(t2, v2, pack2(tanh_coef(k), tanh_coef(k)));
+              float y0, y1;
+              unpack2(v2, y0, y1);
+              far = max3(far, y0, y1);
+              unpack2(mul2(mul2(t2, v), cap2), y0, y1);
+              s[y] = __float_as_uint(y0);
+              s[y + 1] = __float_as_uint(y1);
+            }
+            if (__any_sync(kFull, far > 1.f)) {  // rare: from the raw scores again, which still stand in S
+              tc_ld32(tS + 32 * c, s);
+              tc_wait_ld();
 #pragma unroll
               for (int y = 0; y < 32; ++y) s[y] = __float_as_uint(cap_score(__uint_as_float(s[y]) * p.scale, p.cap));
-            } else {
-#pragma unroll
-              for (int y = 0; y < 32; y += 2) {
-                const uint64_t v = mul2(pack2(__uint_as_float(s[y]), __uint_as_float(s[y + 1])), sc2);
-                const uint64_t v2 = mul2(v, v);
-                uint64_t t2 = pack2(tanh_coef(kTanhTop), tanh_coef(kTanhTop));
-#pragma unroll
-                for (int k = kTanhTop - 1; k >= 0; --k) t2 = fma2(t2, v2, pack2(tanh_coef(k), tanh_coef(k)));
-                float y0, y1;
-                unpack2(mul2(mul2(t2, v), cap2), y0, y1);
-                s[y] = __float_as_uint(y0);
-                s[y + 1] = __float_as_uint(y1);
-              }
             }
           } else {
 #pragma unroll
@@ -535,16 +536,32 @@ __global__ void __launch_bounds__(kDtThreads, 1)
           }
           tc_wait_st();
         };
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          tc_wait_ld();
-          if (!weights(c, sa)) {
+        auto columns = [&](int c, uint32_t (&s)[32]) {
+          if (!weights(c, s)) {
             raise(c);
-            tc_ld32(tS + 32 * c, sa);
+            tc_ld32(tS + 32 * c, s);
             tc_wait_ld();
-            weights(c, sa);  // the largest is 1 now (or NaN)
+            weights(c, s);  // the largest is 1 now (or NaN)
           }
-          if (c < 3) tc_ld32(tS + 32 * (c + 1), sa);
+        };
+        if constexpr (RMAX <= 64) {  // the next columns on their way meanwhile, where registers hold them
+          uint32_t sb[32];
+#pragma unroll 1
+          for (int c = 0; c < 4; c += 2) {
+            tc_wait_ld();
+            tc_ld32(tS + 32 * (c + 1), sb);
+            columns(c, sa);
+            tc_wait_ld();
+            if (c == 0) tc_ld32(tS + 64, sa);
+            columns(c + 1, sb);
+          }
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            tc_wait_ld();
+            columns(c, sa);
+            if (c < 3) tc_ld32(tS + 32 * (c + 1), sa);
+          }
         }
         float sum0, sum1;
         unpack2(total, sum0, sum1);
