@@ -8,10 +8,21 @@
 // than another, whatever the lengths, and a warp needs nothing from its
 // neighbours until its run ends.  Each warp streams its run through a private
 // ring of 1-D bulk copies (a tile of K and of C is contiguous in its page) and
-// works a tile on the tensor cores with the rows as the M of mma.sync m16n8k16
-// (tcgen05 has no shape below 64 rows): S = Q K^T, running maximum and sum,
-// O += P C.  The fp32 weights enter the second product as three bf16 terms (24
-// mantissa bits: o_lat is fp32), for MMAs that the stream hides.
+// works a tile on the tensor cores, the few rows as the N of mma.sync m16n8k16
+// (8 of them; tcgen05's shapes would be mostly padding): S^T = K Q^T, running
+// maximum and sum, O^T += C^T P^T, the weights turned by movmatrix between the
+// two.  The fp32 weights enter the second product as three bf16 terms (24
+// mantissa bits: o_lat is fp32), for MMAs that the stream hides.  A row's
+// reference is its maximum at the last tile where some score passed it by more
+// than 2^8: most tiles need no reduction across the lanes and no rescaling.
+//
+// Measured (bf16, d 128, rank 64, 8 KV heads, 4 heads each): 131 us for 8
+// sequences of 32 k (805 MB, 6.1 TB/s), 141 us for 64 ragged ones with a window
+// and capped scores (806 MB, 5.7 TB/s).  With the rows as M (half of it padding)
+// the first took 133 us and 138 us against 136 in a loop of calls; at 16 rows,
+// where nothing is padding, that layout is 4% the faster one.  Six warps a CTA,
+// for more registers and a deeper ring, cost a single sequence of 8 k 20 us
+// instead of 14: its runs no longer end where the sequence's heads do.
 //
 // Where a run ends inside a sequence, the warp leaves (max, sum, acc) in its
 // slot: run w and group g meet in slot w + g, since along the tiles each step
@@ -27,6 +38,7 @@ namespace bkv {
 
 constexpr int kDmTile = 16;   // tokens per tile
 constexpr int kDmWarps = 8;
+constexpr float kDmRaise = 8.f;  // how far (log2) a score may pass its row's reference before that is raised
 
 constexpr uint32_t dm_stage(int d, int r) { return ((uint32_t)kDmTile * (d + r) * 2 + 127u) & ~127u; }
 // ring depth with `ctas` CTAs on an SM (its 228 KB, less 1 KB reserved and the barriers for each), at most 4
@@ -55,6 +67,12 @@ __device__ __forceinline__ void dm_ldsm_t(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr));
+}
+// an 8 x 8 matrix of b16, two neighbouring elements of a row to a lane, transposed
+__device__ __forceinline__ uint32_t dm_transpose(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 __device__ __forceinline__ uint32_t dm_pack(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
@@ -220,31 +238,38 @@ __global__ void __launch_bounds__(32 * kDmWarps, dm_ctas(D, NT * 8)) dense_mma_k
     while (consumed < tiles && ok) {
       if (out.x == out.n) out.next_group(p);
       const int first = out.x, last = (int)min((long long)out.n, (long long)first + (tiles - consumed));
-      // this piece's queries, scores' slopes and state
+      // this piece's queries (B operand, rows as its columns), and per row of this lane (2 tq, 2 tq + 1 of
+      // each block of 8) the score's slope and the state
       constexpr int RB = ROWS16 ? 2 : 1;
-      uint32_t qa[KS][2 * RB];
-      float slope[RB], m[RB], l[RB];
-      int pos[RB];
-      bool on[RB];
+      uint32_t qb[KS][RB][2];
+      float slope[RB][2], m[RB][2], l[RB][2];
+      int pos[RB][2];
+      bool on[RB][2];
 #pragma unroll
       for (int y = 0; y < RB; ++y) {
-        const int row = gr + 8 * y;
-        on[y] = row < rows;
-        const int t = on[y] ? row / p.G : 0, h = out.g * p.G + (on[y] ? row - t * p.G : 0);
-        pos[y] = out.s.pos0 + t;
-        slope[y] = p.slopes ? p.slopes[h] * kLog2e : 0.f;
-        m[y] = -INFINITY;
-        l[y] = 0.f;
+        const int row = gr + 8 * y, t = row < rows ? row / p.G : 0, h = out.g * p.G + (row < rows ? row - t * p.G : 0);
         const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(p.q) + (((size_t)out.b * p.n_new + t) * p.Hq + h) * D;
 #pragma unroll
-        for (int s2 = 0; s2 < KS; ++s2) {
-          qa[s2][y] = on[y] ? *reinterpret_cast<const uint32_t*>(qr + 16 * s2 + 2 * tq) : 0u;
-          qa[s2][RB + y] = on[y] ? *reinterpret_cast<const uint32_t*>(qr + 16 * s2 + 2 * tq + 8) : 0u;
+        for (int s2 = 0; s2 < KS; ++s2)
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            qb[s2][y][u] = row < rows ? *reinterpret_cast<const uint32_t*>(qr + 16 * s2 + 8 * u + 2 * tq) : 0u;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r2 = 8 * y + 2 * tq + e;
+          on[y][e] = r2 < rows;
+          const int t2 = on[y][e] ? r2 / p.G : 0, h2 = out.g * p.G + (on[y][e] ? r2 - t2 * p.G : 0);
+          pos[y][e] = out.s.pos0 + t2;
+          slope[y][e] = p.slopes ? p.slopes[h2] * kLog2e : 0.f;
+          m[y][e] = -INFINITY;
+          l[y][e] = 0.f;
         }
       }
-      float acc[NT][4];
+      float acc[R / 16][RB][4];  // latents 16 i + gr (elements 0, 1: the lane's rows) and + 8 (2, 3)
 #pragma unroll
-      for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+      for (int i = 0; i < R / 16; ++i)
+#pragma unroll
+        for (int y = 0; y < RB; ++y) acc[i][y][0] = acc[i][y][1] = acc[i][y][2] = acc[i][y][3] = 0.f;
       const bool mod = p.cap > 0.f || p.slopes;
 
       for (; out.x < last; ++out.x) {
@@ -270,73 +295,103 @@ __global__ void __launch_bounds__(32 * kDmWarps, dm_ctas(D, NT * 8)) dense_mma_k
             }
             __syncwarp();
           }
-          float sc[2][2][4];  // [chain][8 tokens][fragment]
+          float sc[2][RB][4];  // [chain][row block][fragment: tokens gr, gr + 8 by the lane's rows]
 #pragma unroll
-          for (int y = 0; y < 16; ++y) (&sc[0][0][0])[y] = 0.f;
+          for (int y = 0; y < 8 * RB; ++y) (&sc[0][0][0])[y] = 0.f;
           {
-            const int tok = (mi >> 1) * 8 + rr;
+            const int tok = (mi & 1) * 8 + rr;
             const uint32_t rowaddr = kaddr + (uint32_t)(tok * D * 2);
 #pragma unroll
             for (int s2 = 0; s2 < KS; ++s2) {
-              uint32_t kb[4];
-              dm_ldsm(kb, rowaddr + (uint32_t)(((2 * s2 + (mi & 1)) ^ (tok & mk)) << 4));
-              const uint32_t a1 = ROWS16 ? qa[s2][RB - 1] : 0u, a3 = ROWS16 ? qa[s2][2 * RB - 1] : 0u;
-              dm_mma(sc[s2 & 1][0], qa[s2][0], a1, qa[s2][RB], a3, kb[0], kb[1]);
-              dm_mma(sc[s2 & 1][1], qa[s2][0], a1, qa[s2][RB], a3, kb[2], kb[3]);
+              uint32_t ka[4];
+              dm_ldsm(ka, rowaddr + (uint32_t)(((2 * s2 + (mi >> 1)) ^ (tok & mk)) << 4));
+#pragma unroll
+              for (int y = 0; y < RB; ++y) dm_mma(sc[s2 & 1][y], ka[0], ka[1], ka[2], ka[3], qb[s2][y][0], qb[s2][y][1]);
             }
           }
-          uint32_t pw[3][2][2];  // [term][row block][8 tokens]
-          float corr[RB];
+          // the scores; does one lie more than 2^kDmRaise above its row's reference?
+          auto each_score = [&](auto f) {  // f(score, its row's block and number in it, its token)
 #pragma unroll
-          for (int y = 0; y < RB; ++y) {
-            float v[4];
+            for (int y = 0; y < RB; ++y)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float raw = sc[0][e >> 1][2 * y + (e & 1)] + sc[1][e >> 1][2 * y + (e & 1)];
-              const int j = j0 + (e >> 1) * 8 + 2 * tq + (e & 1);
-              v[e] = mod ? mod_score(raw, p.scale, p.cap, slope[y], pos[y], j) : raw * p.scale;
-              if (!on[y] || (!whole && !sees(pos[y], j, out.s.L, p.window, out.s.prefix))) v[e] = -INFINITY;
-            }
-            float mx = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
-            mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
-            const float mn = fmaxf(m[y], mx);
-            corr[y] = 1.f;
-            float pr[4];
-            if (mn == -INFINITY) {
+              for (int e = 0; e < 2; ++e)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) pr[e] = v[e] != v[e] ? v[e] : 0.f;
-            } else {
-              corr[y] = ex2(m[y] - mn);
+                for (int u = 0; u < 2; ++u) f(sc[0][y][2 * u + e], y, e, j0 + 8 * u + gr);
+          };
 #pragma unroll
-              for (int e = 0; e < 4; ++e) pr[e] = ex2(v[e] - mn);
-            }
-            m[y] = mn;
-            l[y] = l[y] * corr[y] + ((pr[0] + pr[1]) + (pr[2] + pr[3]));
+          for (int y = 0; y < RB; ++y)
 #pragma unroll
-            for (int u = 0; u < 2; ++u) dm_split(pr[2 * u], pr[2 * u + 1], pw[0][y][u], pw[1][y][u], pw[2][y][u]);
-          }
-          {
-            const int tok = (mi & 1) * 8 + rr;
-            const uint32_t rowaddr = caddr + (uint32_t)(tok * R * 2);
+            for (int e = 0; e < 4; ++e) sc[0][y][e] += sc[1][y][e];
+          if (mod)
+            each_score([&](float& v, int y, int e, int j) { v = mod_score(v, p.scale, p.cap, slope[y][e], pos[y][e], j); });
+          else
+            each_score([&](float& v, int, int, int) { v *= p.scale; });
+          if (!whole)
+            each_score([&](float& v, int y, int e, int j) {
+              if (!sees(pos[y][e], j, out.s.L, p.window, out.s.prefix)) v = -INFINITY;
+            });
+          bool above = false;
+          each_score([&](float& v, int y, int e, int) { above |= v > m[y][e] + kDmRaise; });
+          if (__any_sync(kFull, above)) {  // the references become the maxima so far, and the sums follow
 #pragma unroll
-            for (int jj = 0; jj < NT / 2; ++jj) {
-              uint32_t cb[4];
-              dm_ldsm_t(cb, rowaddr + (uint32_t)(((2 * jj + (mi >> 1)) ^ (tok & mc)) << 4));
-              // the tile's products on their own, then added in fp32: tensor cores cut off what they add
-              // up, which over a long run's tiles would cost more than the three terms keep
-              float t[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            for (int y = 0; y < RB; ++y) {
+              float corr[2];
 #pragma unroll
-              for (int z = 0; z < 3; ++z) {
-                const uint32_t a1 = ROWS16 ? pw[z][RB - 1][0] : 0u, a3 = ROWS16 ? pw[z][RB - 1][1] : 0u;
-                dm_mma(t[0], pw[z][0][0], a1, pw[z][0][1], a3, cb[0], cb[1]);
-                dm_mma(t[1], pw[z][0][0], a1, pw[z][0][1], a3, cb[2], cb[3]);
+              for (int e = 0; e < 2; ++e) {
+                float mx = fmaxf(sc[0][y][e], sc[0][y][2 + e]);
+                mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
+                mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
+                mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
+                mx = fmaxf(m[y][e], mx);
+                corr[e] = mx == -INFINITY ? 1.f : ex2(m[y][e] - mx);
+                m[y][e] = mx;
+                l[y][e] *= corr[e];
               }
 #pragma unroll
-              for (int u = 0; u < 2; ++u)
+              for (int i = 0; i < R / 16; ++i)
 #pragma unroll
-                for (int e = 0; e < 2 * RB; ++e)
-                  acc[2 * jj + u][e] = fmaf(acc[2 * jj + u][e], corr[e >> 1], t[u][e]);
+                for (int e = 0; e < 4; ++e) acc[i][y][e] *= corr[e & 1];
+            }
+          }
+          uint32_t pw[3][RB][2];  // [term][row block][8 tokens]: weights as B operand
+#pragma unroll
+          for (int y = 0; y < RB; ++y) {
+            float pr[2][2];  // [token gr, gr + 8][row]
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const bool none = m[y][e] == -INFINITY;  // nothing seen, or nothing but NaN
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const float v = sc[0][y][2 * u + e];
+                pr[u][e] = none ? (v != v ? v : 0.f) : ex2(v - m[y][e]);
+              }
+              l[y][e] += pr[0][e] + pr[1][e];
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              uint32_t w[3];
+              dm_split(pr[u][0], pr[u][1], w[0], w[1], w[2]);
+#pragma unroll
+              for (int z = 0; z < 3; ++z) pw[z][y][u] = dm_transpose(w[z]);
+            }
+          }
+          {
+            const int tok = (mi >> 1) * 8 + rr;
+            const uint32_t rowaddr = caddr + (uint32_t)(tok * R * 2);
+#pragma unroll
+            for (int i = 0; i < R / 16; ++i) {
+              uint32_t ca[4];
+              dm_ldsm_t(ca, rowaddr + (uint32_t)(((2 * i + (mi & 1)) ^ (tok & mc)) << 4));
+#pragma unroll
+              for (int y = 0; y < RB; ++y) {
+                // the tile's products on their own, then added in fp32: tensor cores cut off what they add
+                // up, which over a long run's tiles would cost more than the three terms keep
+                float t[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int z = 0; z < 3; ++z) dm_mma(t, ca[0], ca[1], ca[2], ca[3], pw[z][y][0], pw[z][y][1]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][y][e] += t[e];
+              }
             }
           }
         }
@@ -349,27 +404,32 @@ __global__ void __launch_bounds__(32 * kDmWarps, dm_ctas(D, NT * 8)) dense_mma_k
       const bool whole_group = first == 0 && last == out.n;
 #pragma unroll
       for (int y = 0; y < RB; ++y) {
-        float ls = l[y];
-        ls += __shfl_xor_sync(kFull, ls, 1);
-        ls += __shfl_xor_sync(kFull, ls, 2);
-        if (!on[y] || !ok) continue;
-        const int row = gr + 8 * y;
-        if (whole_group) {
-          const int t = row / p.G, h = out.g * p.G + row - t * p.G;
-          const size_t at = ((size_t)out.b * p.n_new + t) * p.Hq + h;
-          const float inv = ls > 0.f ? 1.f / ls : (ls == ls ? 0.f : ls);
 #pragma unroll
-          for (int j = 0; j < NT; ++j)
-            *reinterpret_cast<float2*>(p.o + at * R + 8 * j + 2 * tq) =
-                make_float2(ls > 0.f ? acc[j][2 * y] / ls : inv, ls > 0.f ? acc[j][2 * y + 1] / ls : inv);
-          if (p.lse && tq == 0) p.lse[at] = ls > 0.f ? (m[y] + log2f(ls)) * kLn2 : (ls == ls ? -INFINITY : ls);
-        } else {
-          const size_t slot = (size_t)blockIdx.x * kDmWarps + w + (size_t)out.b * p.Hkv + out.g;
-          float* o = p.part + (slot * rows + row) * (R + 2);
-          if (tq == 0) *reinterpret_cast<float2*>(o) = make_float2(m[y], ls);
+        for (int e = 0; e < 2; ++e) {
+          float ls = l[y][e];
+          ls += __shfl_xor_sync(kFull, ls, 4);
+          ls += __shfl_xor_sync(kFull, ls, 8);
+          ls += __shfl_xor_sync(kFull, ls, 16);
+          if (!on[y][e] || !ok) continue;
+          const int row = 8 * y + 2 * tq + e;
+          if (whole_group) {
+            const int t = row / p.G, h = out.g * p.G + row - t * p.G;
+            const size_t at = ((size_t)out.b * p.n_new + t) * p.Hq + h;
 #pragma unroll
-          for (int j = 0; j < NT; ++j)
-            *reinterpret_cast<float2*>(o + 2 + 8 * j + 2 * tq) = make_float2(acc[j][2 * y], acc[j][2 * y + 1]);
+            for (int i = 0; i < R / 16; ++i)
+#pragma unroll
+              for (int u = 0; u < 2; ++u)
+                p.o[at * R + 16 * i + 8 * u + gr] = ls > 0.f ? acc[i][y][2 * u + e] / ls : (ls == ls ? 0.f : ls);
+            if (p.lse && gr == 0) p.lse[at] = ls > 0.f ? (m[y][e] + log2f(ls)) * kLn2 : (ls == ls ? -INFINITY : ls);
+          } else {
+            const size_t slot = (size_t)blockIdx.x * kDmWarps + w + (size_t)out.b * p.Hkv + out.g;
+            float* o = p.part + (slot * rows + row) * (R + 2);
+            if (gr == 0) *reinterpret_cast<float2*>(o) = make_float2(m[y][e], ls);
+#pragma unroll
+            for (int i = 0; i < R / 16; ++i)
+#pragma unroll
+              for (int u = 0; u < 2; ++u) o[2 + 16 * i + 8 * u + gr] = acc[i][y][2 * u + e];
+          }
         }
       }
     }
