@@ -391,8 +391,8 @@ BASISKV_API basiskv_status basiskv_copy(void* dst, const void* src, size_t bytes
  * outside [0, num_phys_pages], BASISKV_DEVERR_BLOCK_TABLE for a page id outside
  * [0, num_phys_pages) in the part of the free list, or the partly filled last
  * page, that it would hand on.
- * Of cfg only page_size is used (all of it is checked).  batch at most 16384
- * (else BASISKV_ERR_UNSUPPORTED).
+ * Of cfg only page_size is used (all of it is checked).  batch at most 16384,
+ * slot_cols at most 2^30 (else BASISKV_ERR_UNSUPPORTED).
  */
 BASISKV_API basiskv_status basiskv_assign_pages(const basiskv_config* cfg, int32_t batch, int32_t max_pages,
                                                 int32_t num_phys_pages, const int32_t* seq_len,
@@ -408,7 +408,8 @@ BASISKV_API basiskv_status basiskv_assign_pages(const basiskv_config* cfg, int32
  * (free_pages holds num_phys_pages entries).  seq_len_out[b] is 0 for a
  * released request and seq_len[b] for the others; free_count_out counts the
  * pages.  block_table is not changed (an entry past a sequence's pages is never
- * read).  In-place use, faults (a page id outside the pool, more free pages than
+ * read).  A page that two requests hold, or that is on the free list already, is
+ * not looked for: it would be on the list twice.  In-place use, faults (a page id outside the pool, more free pages than
  * the pool holds, a bad length: nothing is released) and limits as for
  * basiskv_assign_pages.
  */
@@ -474,6 +475,7 @@ BASISKV_API basiskv_status basiskv_rope_init(basiskv_rope* rope, const basiskv_r
  *   positions (device) [batch][n_new] int32, or NULL: token t of sequence b is
  *     at seq_len[b] - n_new + t, as basiskv_append places it (seq_len (device)
  *     [batch]).  Exactly one of the two is given.
+ * At most 2^31 - 1 tokens (else BASISKV_ERR_UNSUPPORTED).
  * The angle is formed and reduced in fp64, sin and cos and the products are
  * fp32, the result is rounded once to dtype.
  */
@@ -483,7 +485,8 @@ BASISKV_API basiskv_status basiskv_rotary(const basiskv_config* cfg, const basis
                                           int32_t batch, int32_t n_new, void* stream);
 
 /* What a layer's scores are besides scaled dot products.  NULL in place of a
- * pointer to it: the defaults (all zero). */
+ * pointer to it: the defaults (all zero).  scale / softcap (or scale log2 e) has
+ * to be a normal fp32 number and softcap log2 e a finite one. */
 typedef struct {
   float scale;               /* 0: 1 / sqrt(head_dim); else > 0                        */
   float softcap;             /* c > 0: scores become c tanh(s / c); 0: not capped      */
@@ -514,13 +517,15 @@ typedef struct {
  * no new token sees (past the sequence, before every window) are not read.
  * Latents of tokens that some new token of the call sees must be finite (a
  * weight of zero does not stop a NaN); any bits may stand elsewhere.
- * Scores, softmax and sums are fp32; a bf16 cache's weights are multiplied as
- * bf16 pairs (hi + lo, 16 mantissa bits).  Repeated calls on the same inputs
- * give bitwise identical results.
+ * Scores, softmax and sums are fp32; a bf16 cache's weights (rows stored
+ * swizzled) are multiplied as bf16 pairs (hi + lo, 16 mantissa bits), or as
+ * three bf16 terms where n_new * Hq / Hkv is at most 16.  Repeated calls on the
+ * same inputs give bitwise identical results.
  * cache->r_res and cache->summary are not read (they may be NULL).
  * workspace (device): basiskv_dense_attn_workspace_bytes bytes, zero-filled
  * once when it is allocated, and again before it serves another shape; calls
- * that share one must not overlap.  batch at most 65535.
+ * that share one must not overlap.  batch at most 65535; batch * n_new * Hq and
+ * batch * max_pages * P / 16 below 2^31 (else BASISKV_ERR_UNSUPPORTED).
  */
 BASISKV_API basiskv_status basiskv_dense_attn(const basiskv_config* cfg, const basiskv_cache* cache, const void* q,
                                               int32_t batch, int32_t n_new, const basiskv_attn_options* options,

@@ -16,6 +16,7 @@ namespace bkv {
 constexpr int kMaxPagesLimit = 49152;  // route select keeps one key per page in shared memory
 constexpr int kMaxRequests = 16384;    // the pages kernel keeps two words per request in shared memory
 constexpr int kMaxBatch = 65535;       // sequences of a dense_attn grid
+constexpr int kMaxSlotCols = 1 << 30;  // columns of slots are counted in 32 bits, a few past the last
 
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -323,6 +324,7 @@ static basiskv_status pages_common(const basiskv_config* cfg, int32_t batch, int
   if (!seq_len || !amount || !table || !free_pages || !free_count || !seq_len_out || !free_count_out || !err_flag)
     return BASISKV_ERR_INVALID_ARG;
   if (slots && slot_cols <= 0) return BASISKV_ERR_INVALID_ARG;
+  if (slots && slot_cols > kMaxSlotCols) return BASISKV_ERR_UNSUPPORTED;
   // in place: each output over its own input only
   if (amount == seq_len_out || amount == free_count_out || seq_len == free_count_out || free_count == seq_len_out ||
       seq_len_out == free_count_out)
@@ -418,9 +420,17 @@ basiskv_status basiskv_rotary(const basiskv_config* cfg, const basiskv_rope* rop
   const uintptr_t es = esize(cfg);
   for (const void* x : {q, k, (const void*)q_out, (const void*)k_out})
     if (reinterpret_cast<uintptr_t>(x) % es != 0) return BASISKV_ERR_INVALID_ARG;
+  if ((int64_t)batch * n_new > INT32_MAX) return BASISKV_ERR_UNSUPPORTED;  // blocks of the grid
   RotaryParams p{q, k, q_out, k_out, positions, seq_len, q ? q_stride : 0, k ? k_stride : 0, (long long)batch * n_new,
                  n_new, q ? cfg->num_q_heads : 0, k ? cfg->num_kv_heads : 0, cfg->head_dim, rope->rotary_dim, 0, *rope};
   return cuda_status(launch_rotary(p, cfg->dtype == BASISKV_BF16, num_sms(), (cudaStream_t)stream));
+}
+
+// Blocks and tiles of an attention call are counted in 32 bits: those of its rows, and the 16-token tiles
+// that full block tables would hold.
+static bool dense_countable(const basiskv_config* c, int32_t batch, int32_t n_new, int32_t max_pages) {
+  return (int64_t)batch * n_new <= INT32_MAX / c->num_q_heads &&
+         (int64_t)batch * max_pages <= INT32_MAX / (c->page_size / 16);
 }
 
 static DensePlan plan_dense(const basiskv_config* c, int32_t batch, int32_t n_new, int32_t max_pages) {
@@ -430,7 +440,8 @@ static DensePlan plan_dense(const basiskv_config* c, int32_t batch, int32_t n_ne
 
 size_t basiskv_dense_attn_workspace_bytes(const basiskv_config* cfg, int32_t batch, int32_t n_new, int32_t max_pages) {
   if (check_config(cfg) != BASISKV_OK || batch <= 0 || n_new <= 0 || max_pages <= 0 || max_pages > kMaxPagesLimit ||
-      batch > kMaxBatch || (long long)n_new > (long long)max_pages * cfg->page_size)
+      batch > kMaxBatch || (long long)n_new > (long long)max_pages * cfg->page_size ||
+      !dense_countable(cfg, batch, n_new, max_pages))
     return 0;
   return plan_dense(cfg, batch, n_new, max_pages).bytes;
 }
@@ -449,9 +460,14 @@ basiskv_status basiskv_dense_attn(const basiskv_config* cfg, const basiskv_cache
   if ((s = check_cache(cfg, cache, false, false)) != BASISKV_OK) return s;
   if (!q || !o_lat || !err_flag || !aligned16(q) || !aligned16(o_lat)) return BASISKV_ERR_INVALID_ARG;
   if ((long long)n_new > (long long)cache->max_pages * cfg->page_size) return BASISKV_ERR_INVALID_ARG;
+  if (!dense_countable(cfg, batch, n_new, cache->max_pages)) return BASISKV_ERR_UNSUPPORTED;
+  // factors that fp32 does not hold (a cap near its largest value, or near zero) would make every score NaN
+  const double scale = o.scale > 0.f ? (double)o.scale : 1.0 / sqrt((double)cfg->head_dim);
+  const float factor = (float)(o.softcap > 0.f ? scale / o.softcap : scale * 1.4426950408889634);
+  const float cap = (float)((double)o.softcap * 1.4426950408889634);
+  if (!isnormal(factor) || !isfinite(cap)) return BASISKV_ERR_INVALID_ARG;
   const DensePlan pl = plan_dense(cfg, batch, n_new, cache->max_pages);
   if (!ws || ws_bytes < pl.bytes || !aligned16(ws)) return BASISKV_ERR_WORKSPACE;
-  const double scale = o.scale > 0.f ? (double)o.scale : 1.0 / sqrt((double)cfg->head_dim);
   DenseParams p{};
   p.q = q;
   p.k_raw = cache->k_raw;
@@ -475,8 +491,8 @@ basiskv_status basiskv_dense_attn(const basiskv_config* cfg, const basiskv_cache
   p.num_phys = cache->num_phys_pages;
   p.window = o.window;
   p.mc = swz_mask(cfg->rank_v);
-  p.scale = (float)(o.softcap > 0.f ? scale / o.softcap : scale * 1.4426950408889634);
-  p.cap = (float)((double)o.softcap * 1.4426950408889634);
+  p.scale = factor;
+  p.cap = cap;
   return cuda_status(launch_dense_attn(pl, p, cfg->dtype == BASISKV_BF16, ws, (cudaStream_t)stream));
 }
 

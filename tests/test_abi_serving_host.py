@@ -180,6 +180,34 @@ def test_dense_attn_refusals(L):
         assert call(opt=bk.CAttnOptions(**bad)) == BAD, bad
 
 
+def test_counts_past_32_bits_are_refused(L):
+    big = dict(phys=1 << 20, mp=49152)
+    args = (256, 512, 1024, 2048, 4096, 8192, 8448)
+    for cols, want in (((1 << 30) + 1, UNS), ((1 << 31) - 1, UNS)):
+        assert L.basiskv_assign_pages(ctypes.byref(_cfg()), 1, big["mp"], big["phys"], *args, 16384, cols, 32768,
+                                      None) == want
+    rope = bk.CRope()
+    L.basiskv_rope_init(ctypes.byref(rope), ctypes.byref(_params()))
+    assert L.basiskv_rotary(ctypes.byref(_cfg()), ctypes.byref(rope), 256, 4096, None, 0, 131072, None, None, 512,
+                            1 << 16, 1 << 15, None) == UNS
+    c = _cfg(page_size=64)
+    for batch, n, mp in ((65535, 1, 49152), (65535, 4096, 64)):  # tiles of the tables, rows of the call
+        cache = bk.CCache(256, 256, None, None, 256, 256, 1 << 20, mp)
+        assert L.basiskv_dense_attn(ctypes.byref(c), ctypes.byref(cache), 256, batch, n, None, 256, None, 256, 1 << 60,
+                                    256, None) == UNS
+        assert L.basiskv_dense_attn_workspace_bytes(ctypes.byref(c), batch, n, mp) == 0
+    assert L.basiskv_dense_attn_workspace_bytes(ctypes.byref(c), 8192, 1, 49152) > 0
+
+
+@pytest.mark.parametrize("opt", [dict(softcap=1e-44), dict(softcap=3e38), dict(scale=3e38),
+                                 dict(scale=1e-42), dict(scale=1e-30, softcap=1e20)])
+def test_dense_attn_refuses_scores_that_fp32_does_not_hold(L, opt):
+    """scale / softcap, softcap log2(e) and scale log2(e) are fp32 factors in the kernels."""
+    cache = bk.CCache(256, 256, None, None, 256, 256, 10, 10)
+    assert L.basiskv_dense_attn(ctypes.byref(_cfg()), ctypes.byref(cache), 256, 1, 1,
+                                ctypes.byref(bk.CAttnOptions(**opt)), 256, None, 256, 1 << 40, 256, None) == BAD
+
+
 def test_dense_workspace_bytes(L):
     c = ctypes.byref(_cfg())
     assert L.basiskv_dense_attn_workspace_bytes(c, 8, 1, 2048) > 0
