@@ -13,6 +13,13 @@
 // may be the inputs (a captured graph steps in place), and carries each CTA's
 // fault bits to the others, so a call that cannot be met in full changes
 // nothing.
+//
+// Measured (64 requests, pages of 16): 4.1 us for a token each, 13.7 us for
+// prompts of 2048 to 32768 tokens (69 k table entries, 2.1 M slots written),
+// 11.3 us for the release of half of them.  Bound by the latency of a chain of
+// dependent loads: lengths, free count, page ids, then the stores.  A cluster of
+// 16 CTAs (beyond the portable size) took 11.3 and 8.6 us for the last two; it
+// is not used, since a device partitioned for others may not offer it.
 #include "kernels.cuh"
 
 namespace bkv {

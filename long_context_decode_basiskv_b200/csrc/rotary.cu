@@ -11,6 +11,11 @@
 // One angle serves all heads of a token: a CTA computes its tokens' angles
 // once into shared memory, then streams the heads.  The result is rounded
 // once, from fp32 to the storage type.
+//
+// Measured: 110 us for 32767 tokens of 32 + 8 heads of 128 (bf16, slices of a
+// packed projection; 671 MB, 6.1 TB/s, 0.94 of the measured copy rate); 3.6 us
+// for one token of 64 sequences, which is the launch and two dependent loads.
+// Four tokens to a CTA where that still leaves four CTAs for every SM.
 #include "kernels.cuh"
 
 namespace bkv {
