@@ -237,14 +237,6 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   __syncwarp();
 }
 
-// barrier of the 96 threads of warps 9-11: whether `x` holds in all of them
-__device__ __forceinline__ bool all_of_96(bool x) {
-  uint32_t y;
-  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-               "barrier.cta.red.and.pred p, 2, 96, q;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(y) : "r"((uint32_t)x) : "memory");
-  return y != 0;
-}
-
 // bits [lo, hi) of a 32-bit word (bounds of any size)
 __device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
   const uint32_t below_hi = hi >= 32 ? 0xffffffffu : hi <= 0 ? 0u : (1u << hi) - 1u;
@@ -312,7 +304,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
       mbar_init(&kempty[s], 1);
     }
     for (int s = 0; s < CS; ++s) {
-      mbar_init(&cfull[s], 1);
+      mbar_init(&cfull[s], 4);  // from each warp of the two roles that copy C, whichever has the tile
       mbar_init(&cempty[s], 1);
     }
     mbar_init(qfull, two ? 8 : 4);
@@ -691,18 +683,20 @@ __global__ void __launch_bounds__(kDtThreads, 1)
                      ids * p.Hkv + g, &kfull[s]);
           }
         }
-        // (each role waits for every tile's stage, its own or not: a parity says nothing two phases on)
+        // Each role waits for every tile's stage and arrives for every tile, its own or not: a parity says
+        // nothing two phases on, and so the stage cannot be filled and read again before both have passed.
         if (j - 1 >= CS &&
             !warp_wait(&cempty[(j - 1) % CS], (uint32_t)(((j - 1) / CS - 1) & 1))) {
           ok = false;
           break;
         }
-        if (j > 0 && c_by_tma(j - 1, bits_c)) {
+        if (j > 0) {
           const int s = (j - 1) % CS;
-          last_c = j - 1;
-          if (lane == 0) mbar_arrive_expect_tx(&cfull[s], (uint32_t)kDtKeys * r * 2);
+          const bool here = c_by_tma(j - 1, bits_c);
+          if (here) last_c = j - 1;
+          if (lane == 0) mbar_arrive_expect_tx(&cfull[s], here ? (uint32_t)kDtKeys * r * 2 : 0u);
           __syncwarp();
-          if (ids_c >= 0)
+          if (here && ids_c >= 0)
             for (int a = 0; a < r / 64; ++a)
               dt_tma(smem + lay.c + (size_t)s * c_stage + a * kDtAtom + ((lane * 128) << psh), &cmap, a,
                      ids_c * p.Hkv + g, &cfull[s]);
@@ -727,7 +721,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         const uint32_t bits = __ballot_sync(kFull, ids >= 0);
         const int s = j % CS;
         if (j >= CS) {
-          ok = all_of_96(warp_wait(&cempty[s], (uint32_t)((j / CS - 1) & 1)));  // the three warps give up together
+          ok = warp_wait(&cempty[s], (uint32_t)((j / CS - 1) & 1));
           if (!ok) break;
         }
         if (!c_by_tma(j, bits)) {
@@ -754,9 +748,8 @@ __global__ void __launch_bounds__(kDtThreads, 1)
           cp_async_commit_group();
           cp_async_wait_group<0>();
           fence_proxy_async_smem();
-          all_of_96(true);
-          if (ct == 0) mbar_arrive(&cfull[s]);
         }
+        warp_arrive(&cfull[s], lane);
         ids = next;
       }
     } else if (warp == 12 && n > 0) {

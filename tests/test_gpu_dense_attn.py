@@ -110,6 +110,16 @@ def test_long_contexts(name, n, window):
     check(name, [20011, 4097, n], n, window=window)
 
 
+@pytest.mark.parametrize("name,n,batch", [("8b", 130, 7), ("wide", 40, 80), ("r80", 40, 40), ("8b", 96, 13)])
+@pytest.mark.parametrize("mask", [dict(), dict(softcap=30.0, prefix=4000), dict(slopes=True), dict(window=900)])
+def test_more_row_tiles_than_fit_at_once(name, n, batch, mask):
+    """Row tiles in more than one wave, most of them short, the last sequences' long."""
+    lengths = [n + b % 5 for b in range(batch - 4)] + [8200, 700, 8197, 8207]
+    if mask.get("prefix"):
+        mask = dict(mask, prefix=[mask["prefix"]] * batch)
+    check(name, lengths, n, **mask)
+
+
 @pytest.mark.parametrize("name", ["8b", "tiny"])
 def test_block_table_wider_than_the_cache(name):
     """Splits are planned for the table's width; most of them have nothing to do here."""
@@ -253,3 +263,21 @@ def test_lse_joins_two_halves():
     joined = sum(w[x][..., None] * part[x][0] for x in (0, 1))
     assert (joined - o).norm() <= 2.0 ** -15 * o.norm()
     assert (torch.logsumexp(torch.stack([p[1] for p in part]), 0) - lse).abs().max() <= 2.0 ** -15
+
+
+@pytest.mark.parametrize("name,n,L,kw", [("r80", 130, 9000, dict(softcap=30.0, prefix=[8900])),
+                                         ("8b", 130, 9000, dict(window=2000, prefix=[3000]))])
+def test_no_wait_gives_up_over_many_calls(name, n, L, kw):
+    """Calls behind one another, C tiles copied by either of the two roles that copy them (or by one of them
+    throughout): no wait misses its phase, and the results stay bit for bit the same."""
+    cfg = cfg_of(name)
+    cache = Cache(cfg, [L] * 4, 5)
+    kw = {k: v * 4 if k == "prefix" else v for k, v in kw.items()}
+    q, opt = queries(cfg, 4, n, 5), options(cfg, 4, **kw)
+    o, lse, err, ws = run(cfg, cache, q, opt)
+    assert err == 0
+    again, flag = torch.empty_like(o), torch.zeros(1, dtype=torch.int32, device="cuda")
+    for _ in range(200):
+        bk.dense_attn(cfg, cache.paged, q, again, ws, flag, opt)
+    assert int(flag.item()) == 0
+    assert torch.equal(o, again)
