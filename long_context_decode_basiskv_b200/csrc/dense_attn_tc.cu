@@ -237,6 +237,14 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   __syncwarp();
 }
 
+// barrier of the 96 threads of warps 9-11: whether `x` holds in all of them
+__device__ __forceinline__ bool all_of_96(bool x) {
+  uint32_t y;
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+               "barrier.cta.red.and.pred p, 2, 96, q;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(y) : "r"((uint32_t)x) : "memory");
+  return y != 0;
+}
+
 // bits [lo, hi) of a 32-bit word (bounds of any size)
 __device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
   const uint32_t below_hi = hi >= 32 ? 0xffffffffu : hi <= 0 ? 0u : (1u << hi) - 1u;
@@ -268,7 +276,8 @@ __global__ void __launch_bounds__(kDtThreads, 1)
   uint64_t* kempty = kfull + kDtK;
   uint64_t* cfull = kempty + kDtK;
   uint64_t* cempty = cfull + CS;
-  uint64_t* qfull = cempty + CS;
+  uint64_t* cturn = cempty + CS;   // per C stage: free, and its next tile not TMA's
+  uint64_t* qfull = cturn + CS;
   uint64_t* sfull = qfull + 1;     // per S buffer: S there
   uint64_t* pfull = sfull + NB;    // per S buffer: P there, and the O that its product overwrites taken
   uint64_t* ofull = pfull + NB;    // per warpgroup: O there
@@ -304,8 +313,9 @@ __global__ void __launch_bounds__(kDtThreads, 1)
       mbar_init(&kempty[s], 1);
     }
     for (int s = 0; s < CS; ++s) {
-      mbar_init(&cfull[s], 4);  // from each warp of the two roles that copy C, whichever has the tile
+      mbar_init(&cfull[s], 1);
       mbar_init(&cempty[s], 1);
+      mbar_init(&cturn[s], 1);
     }
     mbar_init(qfull, two ? 8 : 4);
     for (int x = 0; x < NB; ++x) {
@@ -683,23 +693,25 @@ __global__ void __launch_bounds__(kDtThreads, 1)
                      ids * p.Hkv + g, &kfull[s]);
           }
         }
-        // Each role waits for every tile's stage and arrives for every tile, its own or not: a parity says
-        // nothing two phases on, and so the stage cannot be filled and read again before both have passed.
-        if (j - 1 >= CS &&
-            !warp_wait(&cempty[(j - 1) % CS], (uint32_t)(((j - 1) / CS - 1) & 1))) {
-          ok = false;
-          break;
-        }
-        if (j > 0) {
+        // A parity says nothing two phases on, so one role only waits for a C stage to be free, for every tile:
+        // this one where any tile may come by TMA, handing the stage on for the others.
+        if (r % 64 == 0 && j > 0) {
           const int s = (j - 1) % CS;
-          const bool here = c_by_tma(j - 1, bits_c);
-          if (here) last_c = j - 1;
-          if (lane == 0) mbar_arrive_expect_tx(&cfull[s], here ? (uint32_t)kDtKeys * r * 2 : 0u);
-          __syncwarp();
-          if (here && ids_c >= 0)
-            for (int a = 0; a < r / 64; ++a)
-              dt_tma(smem + lay.c + (size_t)s * c_stage + a * kDtAtom + ((lane * 128) << psh), &cmap, a,
-                     ids_c * p.Hkv + g, &cfull[s]);
+          if (j - 1 >= CS && !warp_wait(&cempty[s], (uint32_t)(((j - 1) / CS - 1) & 1))) {
+            ok = false;
+            break;
+          }
+          if (c_by_tma(j - 1, bits_c)) {
+            last_c = j - 1;
+            if (lane == 0) mbar_arrive_expect_tx(&cfull[s], (uint32_t)kDtKeys * r * 2);
+            __syncwarp();
+            if (ids_c >= 0)
+              for (int a = 0; a < r / 64; ++a)
+                dt_tma(smem + lay.c + (size_t)s * c_stage + a * kDtAtom + ((lane * 128) << psh), &cmap, a,
+                       ids_c * p.Hkv + g, &cfull[s]);
+          } else {
+            warp_arrive(&cturn[s], lane);
+          }
         }
         ids_c = ids;
         bits_c = bits;
@@ -716,15 +728,21 @@ __global__ void __launch_bounds__(kDtThreads, 1)
       const __nv_bfloat16* cl = static_cast<const __nv_bfloat16*>(p.c_lat);
       const int dr = 96 / cc, dc = 96 - dr * cc;
       int ids = pages_of(0);
+      uint32_t turns = 0;  // bit s: the parity of cturn[s]'s next phase
       for (int j = 0; j < n && ok; ++j) {
         const int next = pages_of(j + 1);
         const uint32_t bits = __ballot_sync(kFull, ids >= 0);
         const int s = j % CS;
-        if (j >= CS) {
-          ok = warp_wait(&cempty[s], (uint32_t)((j / CS - 1) & 1));
-          if (!ok) break;
-        }
         if (!c_by_tma(j, bits)) {
+          bool free = true;
+          if (r % 64 == 0) {  // one phase for each of these tiles, and the last one of this stage was filled here
+            free = warp_wait(&cturn[s], (turns >> s) & 1u);
+            turns ^= 1u << s;
+          } else if (j >= CS) {
+            free = warp_wait(&cempty[s], (uint32_t)((j / CS - 1) & 1));
+          }
+          ok = all_of_96(free);  // the three warps give up together
+          if (!ok) break;
           const int j0 = tile_at(j) * kDtKeys;
           unsigned char* dst = smem + lay.c + (size_t)s * c_stage;
           int row = ct / cc, ch = ct - row * cc;
@@ -748,8 +766,9 @@ __global__ void __launch_bounds__(kDtThreads, 1)
           cp_async_commit_group();
           cp_async_wait_group<0>();
           fence_proxy_async_smem();
+          all_of_96(true);
+          if (ct == 0) mbar_arrive(&cfull[s]);
         }
-        warp_arrive(&cfull[s], lane);
         ids = next;
       }
     } else if (warp == 12 && n > 0) {
