@@ -120,6 +120,23 @@ def test_more_row_tiles_than_fit_at_once(name, n, batch, mask):
     check(name, lengths, n, **mask)
 
 
+@pytest.mark.parametrize("name", list(SHAPES))
+@pytest.mark.parametrize("n", [1, 3, 17, 130])
+@pytest.mark.parametrize("slope", [0.1, -0.1])
+def test_scores_that_rise_or_fall_along_the_keys(name, n, slope):
+    """40 nats from the first key to the last, either way: references are raised, or stand, in every tile."""
+    cfg = cfg_of(name)
+    L = [400, n, 399]
+    cache = Cache(cfg, L, 11)
+    q = queries(cfg, 3, n, 11, 0.5)
+    s = torch.full((cfg.num_q_heads,), slope, device="cuda")
+    o, lse, err, _ = run(cfg, cache, q, bk.AttnOptions(slopes=s))
+    assert err == 0
+    for b in range(3):
+        want = attention(cache.K[b], cache.C[b], q[b], 1 / math.sqrt(cfg.head_dim), slopes=s)
+        assert_attention(o[b], lse[b], *want, f"{name} n={n} slope={slope}")
+
+
 @pytest.mark.parametrize("name", ["8b", "tiny"])
 def test_block_table_wider_than_the_cache(name):
     """Splits are planned for the table's width; most of them have nothing to do here."""
