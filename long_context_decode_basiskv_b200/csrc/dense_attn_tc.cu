@@ -237,6 +237,13 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   __syncwarp();
 }
 
+// named barrier.  0: __syncthreads; 1: the softmax warps; 2: warps 9-11 (below); 3: the CTA, before the registers
+// go back to the launch count
+template <int ID, int THREADS>
+__device__ __forceinline__ void dt_bar() {
+  asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(THREADS) : "memory");
+}
+
 // barrier of the 96 threads of warps 9-11: whether `x` holds in all of them
 __device__ __forceinline__ bool all_of_96(bool x) {
   uint32_t y;
@@ -615,7 +622,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         for (int c = 0; c < RMAX; ++c)
           if (c < r) x[128 * (2 + c)] = acc[c];
       }
-      asm volatile("bar.sync 1, 256;" ::: "memory");
+      dt_bar<1, 256>();
       if (m == 0) {
         const float mo = x[0], lo2 = x[128];
         const float mn = fmaxf(mx, mo);
@@ -646,9 +653,14 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         if (p.lse) p.lse[at] = l > 0.f ? (mx + log2f(l)) * kLn2 : (l == l ? -INFINITY : l);
       }
     }
-    // what follows is common code, for which every warp has the registers it was compiled with
+    // What follows is common code, for which every warp has the registers it was compiled with.  The other
+    // warps take theirs back only behind a barrier of the whole CTA that stands after this branch's release:
+    // taken any earlier, they could be the ones that a softmax warp still waits for at its start.  The
+    // barrier before it brings each warpgroup together between its two changes, as the instruction asks.
     __syncwarp();
+    dt_bar<1, 256>();
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(128));
+    dt_bar<3, kDtThreads>();
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(256 - dt_regs<RMAX>()));
     // physical page of lane x < np of key tile j: -1 where no row sees any of it, or for a bad entry
@@ -825,6 +837,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
       if (!warp_wait(odone, 0)) ok = false;
     }
     __syncwarp();
+    dt_bar<3, kDtThreads>();  // the softmax warps have had their registers and given them back
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(128));
   }
   if (!ok) set_err(p.err, BASISKV_DEVERR_TIMEOUT);
