@@ -522,10 +522,12 @@ typedef struct {
  * three bf16 terms where n_new * Hq / Hkv is at most 16.  Repeated calls on the
  * same inputs give bitwise identical results.
  * cache->r_res and cache->summary are not read (they may be NULL).
- * workspace (device): basiskv_dense_attn_workspace_bytes bytes, zero-filled
- * once when it is allocated, and again before it serves another shape; calls
- * that share one must not overlap.  batch at most 65535; batch * n_new * Hq and
- * batch * max_pages * P / 16 below 2^31 (else BASISKV_ERR_UNSUPPORTED).
+ * workspace (device): basiskv_dense_attn_workspace_bytes bytes at least,
+ * zero-filled once when it is allocated.  It may serve any shapes that need no
+ * more, one after another, without being cleared (its counters stand at the same
+ * place for all and are left at zero); calls that share one must not overlap.
+ * batch at most 65535; batch * n_new * Hq and batch * max_pages * P / 16 below
+ * 2^31 (else BASISKV_ERR_UNSUPPORTED).
  */
 BASISKV_API basiskv_status basiskv_dense_attn(const basiskv_config* cfg, const basiskv_cache* cache, const void* q,
                                               int32_t batch, int32_t n_new, const basiskv_attn_options* options,

@@ -552,7 +552,8 @@ def dense_workspace_bytes(cfg: Config, batch: int, n_new: int, max_pages: int) -
 
 
 def alloc_dense_workspace(cfg: Config, batch: int, n_new: int, max_pages: int, device="cuda") -> torch.Tensor:
-    """A zero-filled workspace of dense_attn for one shape (its counters are left at zero between calls)."""
+    """A zero-filled workspace of dense_attn for this shape and any that needs no more bytes, in any order (its
+    counters are left at zero between calls)."""
     return torch.zeros(max(dense_workspace_bytes(cfg, batch, n_new, max_pages), 256), dtype=torch.uint8, device=device)
 
 

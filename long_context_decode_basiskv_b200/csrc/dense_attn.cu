@@ -260,12 +260,8 @@ DensePlan dense_plan(int batch, int n_new, int Hq, int Hkv, int d, int r, int pa
   const long long units = tiles * Hkv * batch;
   const long long key_tiles = ((long long)max_pages * page + kDcKeys - 1) / kDcKeys;
   pl.splits = (int)std::max(1LL, std::min({2LL * num_sms / units, key_tiles / 2, 256LL}));
-  size_t off = 0;
-  pl.cnt_off = off;
-  off += ((size_t)units * 4 + 255) & ~(size_t)255;
-  pl.part_off = off;
-  if (pl.splits > 1) off += (size_t)units * pl.splits * pl.row_tile * (r + 2) * 4;
-  pl.bytes = (off + 255) & ~(size_t)255;
+  pl.part_off = pl.bytes = dense_counter_bytes(num_sms);
+  if (pl.splits > 1) pl.bytes += ((size_t)units * pl.splits * pl.row_tile * (r + 2) * 4 + 255) & ~(size_t)255;
   return pl;
 }
 
@@ -304,9 +300,8 @@ static cudaError_t launch_core(const DenseParams& p, int row_tile, cudaStream_t 
 }
 
 cudaError_t launch_dense_attn(const DensePlan& pl, DenseParams p, bool bf16, void* scratch, cudaStream_t st) {
-  char* base = static_cast<char*>(scratch);
-  p.cnt = reinterpret_cast<int32_t*>(base + pl.cnt_off);
-  p.part = reinterpret_cast<float*>(base + pl.part_off);
+  p.cnt = static_cast<int32_t*>(scratch);
+  p.part = reinterpret_cast<float*>(static_cast<char*>(scratch) + pl.part_off);
   p.splits = pl.splits;
   if (pl.row_tile == 0) return launch_dense_mma(p, st);
   if (pl.row_tile < 0) return launch_dense_tc(p, st);

@@ -28,7 +28,7 @@ struct DenseParams {
   float* lse;                  // [B][n_new][Hq] or NULL
   int32_t* err;
   float* part;                 // partial results of splits: per row (max, sum, acc[r])
-  int32_t* cnt;                // finished splits of each unit, zero between calls
+  int32_t* cnt;                // finished splits of each row tile, or of each CTA's last group; zero between calls
   int batch, n_new, Hq, Hkv, G, d, r, page, max_pages, num_phys;
   int window;
   int mc;                      // row swizzle of C pages (swz())
@@ -116,13 +116,14 @@ __device__ __forceinline__ int dense_page(const DenseParams& p, int b, int page)
 }
 
 // Counts this CTA among the splits of its unit; true in every thread of the
-// last one, which joins their results.  The counter is left at zero.
+// last one, which joins their results.  The counter is left at zero.  One that
+// did not start there is reported where it shows: below zero, or past the end.
 __device__ __forceinline__ bool dense_last_split(int32_t* cnt, int splits, int32_t* err, int* s_last) {
   __syncthreads();
   if (threadIdx.x == 0) {
     __threadfence();
     const int prev = atomicAdd(cnt, 1);
-    if (prev >= splits) set_err(err, BASISKV_DEVERR_WORKSPACE);
+    if (prev < 0 || prev >= splits) set_err(err, BASISKV_DEVERR_WORKSPACE);
     *s_last = prev == splits - 1;
     if (*s_last) {
       *cnt = 0;

@@ -475,7 +475,8 @@ __global__ void __launch_bounds__(32 * kDmWarps, dm_ctas(D, NT * 8)) dense_mma_k
     if (spans) {
       const long long per_cta = per * kDmWarps;
       const int c0 = (int)(a / per_cta), c1 = (int)((e - 1) / per_cta);
-      if (dense_last_split(p.cnt + slot, c1 - c0 + 1, p.err, &s_last)) {
+      // the counter of its first CTA, of which it is the last group: no other group counts there
+      if (dense_last_split(p.cnt + c0, c1 - c0 + 1, p.err, &s_last)) {
         for (int row = w; row < rows; row += kDmWarps) {
           const size_t at = out_at(row);
           dense_join_row(cta_part + (size_t)(c0 + slot) * pstride + (size_t)row * (R + 2), pstride, c1 - c0 + 1, R,
@@ -497,9 +498,8 @@ static long long dm_grid(int batch, int Hkv, int d, int r, int page, int max_pag
 void dense_plan_mma(DensePlan* pl, int batch, int rows, int Hkv, int d, int r, int page, int max_pages, int num_sms) {
   const long long groups = (long long)batch * Hkv, grid = dm_grid(batch, Hkv, d, r, page, max_pages, num_sms);
   pl->splits = (int)grid;
-  pl->cnt_off = 0;
-  pl->part_off = ((size_t)groups * 4 + 255) & ~(size_t)255;
   const size_t slots = (size_t)(grid * kDmWarps + groups) + (size_t)(grid + groups);
+  pl->part_off = dense_counter_bytes(num_sms);
   pl->bytes = pl->part_off + ((slots * rows * (r + 2) * 4 + 255) & ~(size_t)255);
 }
 

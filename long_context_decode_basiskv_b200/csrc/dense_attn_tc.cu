@@ -864,9 +864,7 @@ void dense_plan_tc(DensePlan* pl, int batch, long long rows, int Hkv, int r, int
   const long long key_tiles = ((long long)max_pages * page + kDtKeys - 1) / kDtKeys;
   // where there are fewer units than SMs, each is split over its keys, four tiles to a split at least
   pl->splits = (int)std::max(1LL, std::min((long long)num_sms / units, key_tiles / 4));
-  pl->cnt_off = 0;
-  pl->part_off = ((size_t)units * 4 + 255) & ~(size_t)255;
-  pl->bytes = pl->part_off;
+  pl->part_off = pl->bytes = dense_counter_bytes(num_sms);
   if (pl->splits > 1) pl->bytes += ((size_t)units * pl->splits * kDtRows * (r + 2) * 4 + 255) & ~(size_t)255;
 }
 

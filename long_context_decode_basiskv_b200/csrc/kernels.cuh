@@ -171,13 +171,18 @@ struct RotaryParams {
 };
 cudaError_t launch_rotary(RotaryParams p, bool bf16, int num_sms, cudaStream_t st);
 
-// Attention over the whole cache: grid and scratch of one call, from the shape only.
+// Attention over the whole cache: grid and scratch of one call, from the shape only.  The scratch begins with the
+// arrival counters, the same bytes of it whatever the shape, so that they are zero for any shape that comes next;
+// behind them stand the partial results.
 struct DensePlan {
   int row_tile;  // rows (new token, head) of a tile; 0: dense_attn_mma.cu,
                  // -1: dense_attn_tc.cu
   int splits;    // shares of the keys; CTAs of dense_attn_mma.cu
-  size_t cnt_off, part_off, bytes;
+  size_t part_off, bytes;
 };
+// Two counters an SM.  dense_attn_mma.cu uses one for each of its CTAs, two an SM at most; the others one for each row
+// tile that is split, and they split none where row tiles outnumber the SMs.
+inline size_t dense_counter_bytes(int num_sms) { return ((size_t)2 * num_sms * sizeof(int32_t) + 255) & ~(size_t)255; }
 struct DenseParams;
 DensePlan dense_plan(int batch, int n_new, int Hq, int Hkv, int d, int r, int page, int max_pages, bool bf16,
                      int num_sms);

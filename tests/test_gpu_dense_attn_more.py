@@ -5,8 +5,8 @@ import math
 import pytest
 import torch
 
-from tests.serving_reference import Cache, assert_attention, attention
-from tests.test_gpu_dense_attn import cfg_of, options, queries, run
+from tests.serving_reference import Cache, assert_attention, attention, swizzle
+from tests.test_gpu_dense_attn import F32, SHAPES, cfg_of, check, options, queries, run
 
 pytestmark = pytest.mark.gpu
 
@@ -32,3 +32,32 @@ def test_many_ctas_without_keys(name, n, empty, pages):
     for _ in range(50):
         bk.dense_attn(cfg, cache.paged, q, again, ws, flag)
     assert int(flag.item()) == 0 and torch.equal(o, again)
+
+
+# ---------------------------------------------------------------------------
+# one workspace, many shapes
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("calls", [
+    # (shape, new tokens, lengths): few CTAs and many, shares of long key axes, in turn
+    [("8b", 1, [9000]), ("8b", 1, [300] * 64), ("8b", 3, [5000, 700]), ("8b", 1, [40] * 200)],
+    [("tiny", 1, [6000]), ("tiny", 1, [300] * 40), ("r24", 2, [5000]), ("f32", 1, [900] * 9)],
+    [("8b", 1, [9000]), ("wide", 130, [4000]), ("8b", 40, [3000]), ("mha", 300, [2000] * 3), ("r80", 1, [500] * 70)],
+    [("wide", 40, [9000]), ("tiny", 1, [2000] * 3), ("8b", 1, [2000] * 30), ("d64", 64, [70] * 50), ("r24", 64, [900])],
+])
+def test_one_workspace_for_many_shapes(calls):
+    """A workspace that holds the largest of several shapes serves them in any order, without being cleared."""
+    cases = []
+    for x, (name, n, lengths) in enumerate(calls):
+        cfg = cfg_of(name)
+        cache = Cache(cfg, lengths, 20 + x)
+        q = queries(cfg, len(lengths), n, 20 + x)
+        o, lse, err, _ = run(cfg, cache, q, None)          # a workspace of its own
+        assert err == 0
+        cases.append((cfg, cache, q, o, lse, bk.dense_workspace_bytes(cfg, len(lengths), n, cache.max_pages)))
+    ws = torch.zeros(max(c[-1] for c in cases), dtype=torch.uint8, device="cuda")
+    for turn in range(3):
+        for x in (range(len(cases)) if turn != 1 else reversed(range(len(cases)))):
+            cfg, cache, q, o, lse, _ = cases[x]
+            o2, lse2, err, _ = run(cfg, cache, q, None, ws)  # (o2 and lse2 start as NaN)
+            assert err == 0
+            assert torch.equal(o, o2) and torch.equal(lse, lse2), (turn, calls[x])
