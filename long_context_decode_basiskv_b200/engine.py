@@ -17,9 +17,15 @@ beside the append as its programmatic dependent, one stream) or "streams"
 (append, dense_attn with ``options``, out_proj).  ``rope`` rotates the step's
 queries and keys, and the prefilled keys, by their positions before they are
 used.  ``paging`` "pool" takes the block table from a PagePool on the device
-instead of from the case.
+instead of from the case: once, when the engine is built (``step`` is one step
+of the case's lengths; a loop whose requests grow and end calls the pool).
+
+With a ``stream`` the build and its temporaries are on that stream, behind what
+the current stream holds, and the current stream goes on behind the build.
 """
 from __future__ import annotations
+
+import contextlib
 
 import torch
 
@@ -35,6 +41,18 @@ def config_of(case: Case) -> bk.Config:
 
 
 _GROUP_REDUCE = {"group_sum": bk.GROUP_SUM, "group_max": bk.GROUP_MAX}
+
+
+@contextlib.contextmanager
+def _torch_on(stream):
+    """torch's own work (fills, copies) and the memory of its temporaries on `stream`, like the library calls
+    that read them: behind what the current stream holds.  None: nothing changes."""
+    if stream is None:
+        yield
+        return
+    stream.wait_stream(torch.cuda.current_stream(stream.device))
+    with torch.cuda.stream(stream):
+        yield
 
 
 class DecodeEngine:
@@ -58,9 +76,16 @@ class DecodeEngine:
         self.routing = routing
         self.prefill_mode = prefill_mode
         self.case = case
-        self.cfg = cfg = config_of(case)
+        self.cfg = config_of(case)
         self.device = torch.device(device)
-        dev = self.device
+        with _torch_on(stream):
+            self._build(paging, stream)
+        if stream is not None:
+            torch.cuda.current_stream(stream.device).wait_stream(stream)
+
+    def _build(self, paging: str, stream):
+        case, cfg, dev = self.case, self.cfg, self.device
+        attention, rope = self.attention, self.rope
         B = case.wl.batch
         lengths = torch.tensor(case.lengths, dtype=torch.int32)
         self.err = torch.zeros(1, dtype=torch.int32, device=dev)
@@ -104,7 +129,7 @@ class DecodeEngine:
         self.sel_cnt = torch.empty((B, cfg.num_q_heads), dtype=torch.int32, device=dev)
         self.o_lat = torch.empty((B, cfg.num_q_heads, cfg.rank_v), dtype=torch.float32, device=dev)
         self.y = torch.empty((B, cfg.hidden), dtype=torch.float32, device=dev)
-        self.prefill(stream)
+        self._prefill(stream)
 
     def input_buffer(self) -> torch.Tensor:
         """The device buffer holding q, k_new and v_new back to back (in that order)."""
@@ -112,6 +137,10 @@ class DecodeEngine:
 
     def prefill(self, stream=None):
         """Append every token but the last of each sequence (one call per sequence)."""
+        with _torch_on(stream):
+            self._prefill(stream)
+
+    def _prefill(self, stream):
         cfg, case = self.cfg, self.case
         dev = self.device
         for b, L in enumerate(case.lengths):

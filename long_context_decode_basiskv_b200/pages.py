@@ -3,7 +3,14 @@
 ``PagePool`` owns the free list and steps a batch's lengths and block table in
 place with the library's page calls, so that a decode step captured in a CUDA
 graph allocates its own pages: ``extend`` before the append of new tokens,
-``release`` when requests end.
+``release`` when requests end.  A released request holds no token, and
+basiskv_append takes a length below its new tokens for a fault: it leaves the
+batch, or gets tokens from ``extend``, before the next append.
+
+The pool's tensors are made on the current stream.  ``extend`` and ``release``
+run on ``stream`` (default: the current one); a caller that gives one orders it
+behind the pool's making, and keeps ``add_len`` or ``release`` from being
+written over or freed before the call has run.
 """
 from __future__ import annotations
 
