@@ -144,14 +144,18 @@ class Config:
         return self.num_q_heads // self.num_kv_heads
 
     def c(self) -> CConfig:
-        """The C struct (made once: no call writes to it)."""
+        """The C struct, a new one every time."""
+        return CConfig(self.num_q_heads, self.num_kv_heads, self.head_dim, self.rank_v, self.rank_k,
+                       self.page_size, self.hidden, self.top_k,
+                       BF16 if self.dtype == torch.bfloat16 else F32)
+
+    def _ref(self):
+        """The C struct as the calls here pass it: made once, written to by none of them, not handed out."""
         made = self.__dict__.get("_c")
         if made is None:
-            made = CConfig(self.num_q_heads, self.num_kv_heads, self.head_dim, self.rank_v, self.rank_k,
-                           self.page_size, self.hidden, self.top_k,
-                           BF16 if self.dtype == torch.bfloat16 else F32)
+            made = self.c()
             object.__setattr__(self, "_c", made)
-        return made
+        return ctypes.byref(made)
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -243,7 +247,7 @@ class Factors:
 
 
 def workspace_bytes(cfg: Config, batch: int, max_pages: int) -> int:
-    return int(lib().basiskv_workspace_bytes(ctypes.byref(cfg.c()), batch, max_pages))
+    return int(lib().basiskv_workspace_bytes(cfg._ref(), batch, max_pages))
 
 
 def alloc_workspace(cfg: Config, batch: int, max_pages: int, device="cuda") -> torch.Tensor:
@@ -255,7 +259,7 @@ def fuse_out_factor(cfg: Config, Bf: torch.Tensor, W_O: torch.Tensor, Gt: torch.
     _need(Bf, "Bf", cfg.dtype, (cfg.num_kv_heads, cfg.rank_v, cfg.head_dim))
     _need(W_O, "W_O", cfg.dtype, (cfg.num_q_heads * cfg.head_dim, cfg.hidden))
     _need(Gt, "Gt", cfg.dtype, (cfg.hidden, cfg.num_q_heads, cfg.rank_v))
-    _check(lib().basiskv_fuse_out_factor(ctypes.byref(cfg.c()), _ptr(Bf), _ptr(W_O), _ptr(Gt),
+    _check(lib().basiskv_fuse_out_factor(cfg._ref(), _ptr(Bf), _ptr(W_O), _ptr(Gt),
                                          _stream(stream)), "basiskv_fuse_out_factor")
 
 
@@ -267,7 +271,7 @@ def append(cfg: Config, cache: PagedCache, f: Factors, k_new: torch.Tensor, v_ne
     _need(k_new, "k_new", cfg.dtype, shape)
     _need(v_new, "v_new", cfg.dtype, shape)
     _need(err, "err", torch.int32)
-    _check(lib().basiskv_append(ctypes.byref(cfg.c()), ctypes.byref(cache.c()), ctypes.byref(f.c()),
+    _check(lib().basiskv_append(cfg._ref(), ctypes.byref(cache.c()), ctypes.byref(f.c()),
                                 _ptr(k_new), _ptr(v_new), B, n_new, _ptr(err), _stream(stream)),
            "basiskv_append")
 
@@ -280,7 +284,7 @@ def prefill(cfg: Config, cache: PagedCache, f: Factors, k_new: torch.Tensor, v_n
     _need(k_new, "k_new", cfg.dtype, shape)
     _need(v_new, "v_new", cfg.dtype, shape)
     _need(err, "err", torch.int32)
-    _check(lib().basiskv_prefill(ctypes.byref(cfg.c()), ctypes.byref(cache.c()), ctypes.byref(f.c()),
+    _check(lib().basiskv_prefill(cfg._ref(), ctypes.byref(cache.c()), ctypes.byref(f.c()),
                                  _ptr(k_new), _ptr(v_new), B, n_new, _ptr(err), _stream(stream)),
            "basiskv_prefill")
 
@@ -295,7 +299,7 @@ def route(cfg: Config, cache: PagedCache, q: torch.Tensor, sel: torch.Tensor, se
     _need(err, "err", torch.int32)
     if scores is not None:
         _need(scores, "scores", torch.float32, (B, cfg.num_q_heads, cache.max_pages))
-    _check(lib().basiskv_route(ctypes.byref(cfg.c()), ctypes.byref(cache.c()), _ptr(q), B, _ptr(sel),
+    _check(lib().basiskv_route(cfg._ref(), ctypes.byref(cache.c()), _ptr(q), B, _ptr(sel),
                                _ptr(sel_cnt), _ptr(scores), _ptr(ws), ws.numel(), _ptr(err),
                                _stream(stream)), "basiskv_route")
 
@@ -313,7 +317,7 @@ def append_route(cfg: Config, cache: PagedCache, f: Factors, k_new: torch.Tensor
     _need(sel_cnt, "sel_cnt", torch.int32, (B, cfg.num_q_heads))
     _need(ws, "workspace", torch.uint8)
     _need(err, "err", torch.int32)
-    _check(lib().basiskv_append_route(ctypes.byref(cfg.c()), ctypes.byref(cache.c()), ctypes.byref(f.c()),
+    _check(lib().basiskv_append_route(cfg._ref(), ctypes.byref(cache.c()), ctypes.byref(f.c()),
                                       _ptr(k_new), _ptr(v_new), _ptr(q), B, reduce, _ptr(sel), _ptr(sel_cnt),
                                       _ptr(ws), ws.numel(), _ptr(err), _stream(stream)), "basiskv_append_route")
 
@@ -331,7 +335,7 @@ def route_group(cfg: Config, cache: PagedCache, q: torch.Tensor, reduce: int, se
     _need(err, "err", torch.int32)
     if scores is not None:
         _need(scores, "scores", torch.float32, (B, cfg.num_kv_heads, cache.max_pages))
-    _check(lib().basiskv_route_group(ctypes.byref(cfg.c()), ctypes.byref(cache.c()), _ptr(q), B, reduce,
+    _check(lib().basiskv_route_group(cfg._ref(), ctypes.byref(cache.c()), _ptr(q), B, reduce,
                                      _ptr(sel), _ptr(sel_cnt), _ptr(scores), _ptr(ws), ws.numel(),
                                      _ptr(err), _stream(stream)), "basiskv_route_group")
 
@@ -351,7 +355,7 @@ def decode_attn(cfg: Config, cache: PagedCache, q: torch.Tensor, sel: Optional[t
     _need(o_lat, "o_lat", torch.float32, (B, cfg.num_q_heads, cfg.rank_v))
     _need(ws, "workspace", torch.uint8)
     _need(err, "err", torch.int32)
-    _check(lib().basiskv_decode_attn(ctypes.byref(cfg.c()), ctypes.byref(cache.c()), _ptr(q), B,
+    _check(lib().basiskv_decode_attn(cfg._ref(), ctypes.byref(cache.c()), _ptr(q), B,
                                      _ptr(sel), _ptr(sel_cnt), _ptr(o_lat), _ptr(ws), ws.numel(),
                                      _ptr(err), _stream(stream)), "basiskv_decode_attn")
 
@@ -362,7 +366,7 @@ def out_proj(cfg: Config, f: Factors, o_lat: torch.Tensor, y: torch.Tensor, ws: 
     _need(o_lat, "o_lat", torch.float32, (B, cfg.num_q_heads, cfg.rank_v))
     _need_reachable(y, "y", torch.float32, (B, cfg.hidden))  # device, or pinned host: stored there directly
     _need(ws, "workspace", torch.uint8)
-    _check(lib().basiskv_out_proj(ctypes.byref(cfg.c()), ctypes.byref(f.c()), _ptr(o_lat), B, _ptr(y),
+    _check(lib().basiskv_out_proj(cfg._ref(), ctypes.byref(f.c()), _ptr(o_lat), B, _ptr(y),
                                   _ptr(ws), ws.numel(), _stream(stream)), "basiskv_out_proj")
 
 
@@ -387,7 +391,7 @@ def decode_attn_noalloc(cfg: Config, cache: PagedCache, q: torch.Tensor, sel: to
     _need(sel_cnt, "sel_cnt", torch.int32, (B, cfg.num_q_heads))
     _need(o_lat, "o_lat", torch.float32, (B, cfg.num_q_heads, cfg.rank_v))
     _need(err, "err", torch.int32)
-    _check(lib().basiskv_decode_attn_noalloc(ctypes.byref(cfg.c()), ctypes.byref(cache.c()), _ptr(q), B,
+    _check(lib().basiskv_decode_attn_noalloc(cfg._ref(), ctypes.byref(cache.c()), _ptr(q), B,
                                              _ptr(sel), _ptr(sel_cnt), _ptr(o_lat), _ptr(err),
                                              _stream(stream)), "basiskv_decode_attn_noalloc")
 
@@ -424,7 +428,7 @@ def assign_pages(cfg: Config, block_table: torch.Tensor, seq_len: torch.Tensor, 
     if slots is not None:
         _need(slots, "slots", i32, (B, slots.shape[1]) if slots.dim() == 2 else (B, -1))
     _same_device(seq_len, block_table, add_len, free_pages, free_count, seq_len_out, free_count_out, slots, err)
-    _check(lib().basiskv_assign_pages(ctypes.byref(cfg.c()), B, max_pages, free_pages.numel(), _ptr(seq_len),
+    _check(lib().basiskv_assign_pages(cfg._ref(), B, max_pages, free_pages.numel(), _ptr(seq_len),
                                       _ptr(add_len), _ptr(block_table), _ptr(free_pages), _ptr(free_count),
                                       _ptr(seq_len_out), _ptr(free_count_out), _ptr(slots),
                                       0 if slots is None else slots.shape[1], _ptr(err), _stream(stream)),
@@ -449,7 +453,7 @@ def release_pages(cfg: Config, block_table: torch.Tensor, seq_len: torch.Tensor,
     _need(free_count_out, "free_count_out", i32, (1,))
     _need(err, "err", i32)
     _same_device(seq_len, block_table, release, free_pages, free_count, seq_len_out, free_count_out, err)
-    _check(lib().basiskv_release_pages(ctypes.byref(cfg.c()), B, max_pages, free_pages.numel(), _ptr(seq_len),
+    _check(lib().basiskv_release_pages(cfg._ref(), B, max_pages, free_pages.numel(), _ptr(seq_len),
                                        _ptr(release), _ptr(block_table), _ptr(free_pages), _ptr(free_count),
                                        _ptr(seq_len_out), _ptr(free_count_out), _ptr(err), _stream(stream)),
            "basiskv_release_pages")
@@ -532,7 +536,7 @@ def rotary(cfg: Config, rope: Rope, q: Optional[torch.Tensor], k: Optional[torch
     else:
         _need(seq_len, "seq_len", torch.int32, (B,))
     _same_device(first, q, k, q_out, k_out, positions, seq_len)
-    _check(lib().basiskv_rotary(ctypes.byref(cfg.c()), ctypes.byref(rope.c), _ptr(q), strides[0], _ptr(k), strides[1],
+    _check(lib().basiskv_rotary(cfg._ref(), ctypes.byref(rope.c), _ptr(q), strides[0], _ptr(k), strides[1],
                                 _ptr(q_out), _ptr(k_out), _ptr(positions), _ptr(seq_len), B, n, _stream(stream)),
            "basiskv_rotary")
 
@@ -548,7 +552,7 @@ class AttnOptions:
 
 
 def dense_workspace_bytes(cfg: Config, batch: int, n_new: int, max_pages: int) -> int:
-    return int(lib().basiskv_dense_attn_workspace_bytes(ctypes.byref(cfg.c()), batch, n_new, max_pages))
+    return int(lib().basiskv_dense_attn_workspace_bytes(cfg._ref(), batch, n_new, max_pages))
 
 
 def alloc_dense_workspace(cfg: Config, batch: int, n_new: int, max_pages: int, device="cuda") -> torch.Tensor:
@@ -584,5 +588,5 @@ def dense_attn(cfg: Config, cache: PagedCache, q: torch.Tensor, o_lat: torch.Ten
             _need(prefix, "prefix_len", torch.int32, (B,))
         opt = ctypes.byref(CAttnOptions(options.scale, options.softcap, options.window, 0, _ptr(slopes), _ptr(prefix)))
     _same_device(q, cache.k_raw, o_lat, ws, err, lse, slopes, prefix)
-    _check(lib().basiskv_dense_attn(ctypes.byref(cfg.c()), ctypes.byref(cache.c()), _ptr(q), B, n, opt, _ptr(o_lat),
+    _check(lib().basiskv_dense_attn(cfg._ref(), ctypes.byref(cache.c()), _ptr(q), B, n, opt, _ptr(o_lat),
                                     _ptr(lse), _ptr(ws), ws.numel(), _ptr(err), _stream(stream)), "basiskv_dense_attn")
