@@ -587,6 +587,6 @@ def dense_attn(cfg: Config, cache: PagedCache, q: torch.Tensor, o_lat: torch.Ten
         if prefix is not None:
             _need(prefix, "prefix_len", torch.int32, (B,))
         opt = ctypes.byref(CAttnOptions(options.scale, options.softcap, options.window, 0, _ptr(slopes), _ptr(prefix)))
-    _same_device(q, cache.k_raw, o_lat, ws, err, lse, slopes, prefix)
+    _same_device(q, cache.k_raw, cache.c_lat, cache.block_table, cache.seq_len, o_lat, ws, err, lse, slopes, prefix)
     _check(lib().basiskv_dense_attn(cfg._ref(), ctypes.byref(cache.c()), _ptr(q), B, n, opt, _ptr(o_lat),
                                     _ptr(lse), _ptr(ws), ws.numel(), _ptr(err), _stream(stream)), "basiskv_dense_attn")

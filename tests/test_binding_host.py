@@ -27,3 +27,57 @@ def test_a_config_hands_out_structs_of_its_own():
     assert cfg._ref()._obj.head_dim == 64
     for other in (copy.deepcopy(cfg), pickle.loads(pickle.dumps(cfg))):     # after a call has made the struct
         assert other == cfg and other._ref()._obj.page_size == 16
+
+
+class Stand:
+    """What the binding asks of a tensor before it calls the library, without a GPU."""
+
+    def __init__(self, shape, device=0):
+        self.shape, self.at = torch.Size(shape), device
+        self.device = f"cuda:{device}" if device >= 0 else "cpu"
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return self.shape.numel()
+
+    def get_device(self):
+        return self.at
+
+    def data_ptr(self):
+        return 256
+
+
+@pytest.fixture
+def no_library(monkeypatch):
+    calls = []
+    monkeypatch.setattr(bk, "_need", lambda *a, **kw: None)
+    monkeypatch.setattr(bk, "_stream", lambda s: None)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *a: calls.append(name) or bk.OK
+    monkeypatch.setattr(bk, "lib", Library)
+    return calls
+
+
+def cache_of_stands(**at):
+    cache = bk.PagedCache.__new__(bk.PagedCache)
+    cache.num_phys_pages = 4
+    for name, shape in (("k_raw", (4, 2, 16, 64)), ("c_lat", (4, 2, 16, 16)), ("r_res", (4, 2, 16, 8)),
+                        ("summary", (4, 2, 64)), ("block_table", (1, 4)), ("seq_len", (1,))):
+        setattr(cache, name, Stand(shape, at.get(name, 0)))
+    return cache
+
+
+@pytest.mark.parametrize("name", ["k_raw", "c_lat", "block_table", "seq_len"])
+@pytest.mark.parametrize("device", [1, -1])
+def test_attention_over_a_cache_on_another_device(no_library, name, device):
+    args = Stand((1, 8, 64)), Stand((1, 8, 16)), Stand((4096,)), Stand((1,))
+    bk.dense_attn(config(), cache_of_stands(), *args)
+    assert no_library == ["basiskv_dense_attn"]
+    with pytest.raises(ValueError, match="others are on cuda:0"):
+        bk.dense_attn(config(), cache_of_stands(**{name: device}), *args)
+    assert len(no_library) == 1
