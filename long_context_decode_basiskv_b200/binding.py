@@ -158,6 +158,9 @@ class Config:
         return ctypes.byref(made)
 
 
+_I32 = 2 ** 31 - 1  # ctypes takes a larger number's low 32 bits; this one the library takes, or refuses
+
+
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
@@ -428,10 +431,10 @@ def assign_pages(cfg: Config, block_table: torch.Tensor, seq_len: torch.Tensor, 
     if slots is not None:
         _need(slots, "slots", i32, (B, slots.shape[1]) if slots.dim() == 2 else (B, -1))
     _same_device(seq_len, block_table, add_len, free_pages, free_count, seq_len_out, free_count_out, slots, err)
-    _check(lib().basiskv_assign_pages(cfg._ref(), B, max_pages, free_pages.numel(), _ptr(seq_len),
+    _check(lib().basiskv_assign_pages(cfg._ref(), B, max_pages, min(free_pages.numel(), _I32), _ptr(seq_len),
                                       _ptr(add_len), _ptr(block_table), _ptr(free_pages), _ptr(free_count),
                                       _ptr(seq_len_out), _ptr(free_count_out), _ptr(slots),
-                                      0 if slots is None else slots.shape[1], _ptr(err), _stream(stream)),
+                                      0 if slots is None else min(slots.shape[1], _I32), _ptr(err), _stream(stream)),
            "basiskv_assign_pages")
 
 
@@ -453,7 +456,7 @@ def release_pages(cfg: Config, block_table: torch.Tensor, seq_len: torch.Tensor,
     _need(free_count_out, "free_count_out", i32, (1,))
     _need(err, "err", i32)
     _same_device(seq_len, block_table, release, free_pages, free_count, seq_len_out, free_count_out, err)
-    _check(lib().basiskv_release_pages(cfg._ref(), B, max_pages, free_pages.numel(), _ptr(seq_len),
+    _check(lib().basiskv_release_pages(cfg._ref(), B, max_pages, min(free_pages.numel(), _I32), _ptr(seq_len),
                                        _ptr(release), _ptr(block_table), _ptr(free_pages), _ptr(free_count),
                                        _ptr(seq_len_out), _ptr(free_count_out), _ptr(err), _stream(stream)),
            "basiskv_release_pages")
@@ -546,7 +549,7 @@ class AttnOptions:
     """What a layer's scores are besides scaled dot products (basiskv_attn_options)."""
     scale: float = 0.0                          # 0: 1 / sqrt(head_dim)
     softcap: float = 0.0                        # c > 0: c tanh(s / c)
-    window: int = 0                             # w > 0: the last w tokens, itself included
+    window: int = 0                             # w > 0: the last w tokens, itself included (however large)
     slopes: Optional[torch.Tensor] = None       # [Hq] fp32: slope * distance is taken off
     prefix_len: Optional[torch.Tensor] = None   # [B] int32: tokens that every new token sees
 
@@ -586,7 +589,11 @@ def dense_attn(cfg: Config, cache: PagedCache, q: torch.Tensor, o_lat: torch.Ten
             _need(slopes, "slopes", torch.float32, (cfg.num_q_heads,))
         if prefix is not None:
             _need(prefix, "prefix_len", torch.int32, (B,))
-        opt = ctypes.byref(CAttnOptions(options.scale, options.softcap, options.window, 0, _ptr(slopes), _ptr(prefix)))
+        opt = CAttnOptions(options.scale, options.softcap, max(-1, min(options.window, _I32)), 0, _ptr(slopes),
+                           _ptr(prefix))
+        if (opt.scale == 0 and options.scale != 0) or (opt.softcap == 0 and options.softcap != 0):
+            raise ValueError(f"scale {options.scale} or softcap {options.softcap} is 0 in fp32, which stands for none")
+        opt = ctypes.byref(opt)
     _same_device(q, cache.k_raw, cache.c_lat, cache.block_table, cache.seq_len, o_lat, ws, err, lse, slopes, prefix)
     _check(lib().basiskv_dense_attn(cfg._ref(), ctypes.byref(cache.c()), _ptr(q), B, n, opt, _ptr(o_lat),
                                     _ptr(lse), _ptr(ws), ws.numel(), _ptr(err), _stream(stream)), "basiskv_dense_attn")

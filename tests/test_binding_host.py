@@ -81,3 +81,40 @@ def test_attention_over_a_cache_on_another_device(no_library, name, device):
     with pytest.raises(ValueError, match="others are on cuda:0"):
         bk.dense_attn(config(), cache_of_stands(**{name: device}), *args)
     assert len(no_library) == 1
+
+
+@pytest.fixture
+def passed(no_library, monkeypatch):
+    """The arguments of the library's calls."""
+    seen = []
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *a: seen.append(a) or bk.OK
+    monkeypatch.setattr(bk, "lib", Library)
+    return seen
+
+
+@pytest.mark.parametrize("window,want", [(5, 5), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31, 2 ** 31 - 1),
+                                         (2 ** 32, 2 ** 31 - 1), (2 ** 32 + 7, 2 ** 31 - 1), (-3, -1), (-2 ** 32, -1)])
+def test_a_window_past_32_bits_is_no_smaller_one(passed, window, want):
+    args = Stand((1, 8, 64)), Stand((1, 8, 16)), Stand((4096,)), Stand((1,))
+    bk.dense_attn(config(), cache_of_stands(), *args, bk.AttnOptions(window=window))
+    assert passed[0][5]._obj.window == want
+
+
+@pytest.mark.parametrize("opt", [dict(scale=1e-50), dict(softcap=1e-60), dict(scale=-1e-50)])
+def test_options_that_fp32_makes_zero_are_refused(passed, opt):
+    """Zero stands for the default scale, or for no cap."""
+    args = Stand((1, 8, 64)), Stand((1, 8, 16)), Stand((4096,)), Stand((1,))
+    with pytest.raises(ValueError, match="fp32"):
+        bk.dense_attn(config(), cache_of_stands(), *args, bk.AttnOptions(**opt))
+    assert not passed
+
+
+def test_counts_past_32_bits_are_not_cut_off(passed):
+    i = Stand((1,))
+    bk.assign_pages(config(), Stand((1, 4)), i, i, Stand((2 ** 32 + 5,)), i, i, i, Stand((1, 2 ** 32 + 8)), i)
+    assert passed[0][3] == passed[0][12] == 2 ** 31 - 1
+    bk.release_pages(config(), Stand((1, 4)), i, i, Stand((2 ** 32 + 5,)), i, i, i, i)
+    assert passed[1][3] == 2 ** 31 - 1
