@@ -392,7 +392,8 @@ BASISKV_API basiskv_status basiskv_copy(void* dst, const void* src, size_t bytes
  * [0, num_phys_pages) in the part of the free list, or the partly filled last
  * page, that it would hand on.
  * Of cfg only page_size is used (all of it is checked).  batch at most 16384,
- * slot_cols at most 2^30 (else BASISKV_ERR_UNSUPPORTED).
+ * slot_cols at most 2^30 (else BASISKV_ERR_UNSUPPORTED).  batch 0 is no error:
+ * nothing is read or written, free_count_out neither.
  */
 BASISKV_API basiskv_status basiskv_assign_pages(const basiskv_config* cfg, int32_t batch, int32_t max_pages,
                                                 int32_t num_phys_pages, const int32_t* seq_len,
@@ -409,9 +410,9 @@ BASISKV_API basiskv_status basiskv_assign_pages(const basiskv_config* cfg, int32
  * released request and seq_len[b] for the others; free_count_out counts the
  * pages.  block_table is not changed (an entry past a sequence's pages is never
  * read).  A page that two requests hold, or that is on the free list already, is
- * not looked for: it would be on the list twice.  In-place use, faults (a page id outside the pool, more free pages than
- * the pool holds, a bad length: nothing is released) and limits as for
- * basiskv_assign_pages.
+ * not looked for: it would be on the list twice.  In-place use, faults (a page
+ * id outside the pool, more free pages than the pool holds, a bad length: nothing
+ * is released), limits and an empty batch as for basiskv_assign_pages.
  */
 BASISKV_API basiskv_status basiskv_release_pages(const basiskv_config* cfg, int32_t batch, int32_t max_pages,
                                                  int32_t num_phys_pages, const int32_t* seq_len,

@@ -409,6 +409,13 @@ def _same_device(first: torch.Tensor, *others: Optional[torch.Tensor]):
             raise ValueError(f"a tensor is on {t.device}, the others are on cuda:{d}")
 
 
+def _same_count(free_count_out: torch.Tensor, free_count: torch.Tensor, stream):
+    """What a page call leaves as the free list's count for an empty batch, for which the library writes nothing."""
+    if free_count_out.data_ptr() != free_count.data_ptr():
+        with torch.cuda.stream(stream):  # (None: the current one)
+            free_count_out.copy_(free_count)
+
+
 def assign_pages(cfg: Config, block_table: torch.Tensor, seq_len: torch.Tensor, add_len: torch.Tensor,
                  free_pages: torch.Tensor, free_count: torch.Tensor, seq_len_out: torch.Tensor,
                  free_count_out: torch.Tensor, slots: Optional[torch.Tensor], err: torch.Tensor, stream=None):
@@ -431,6 +438,8 @@ def assign_pages(cfg: Config, block_table: torch.Tensor, seq_len: torch.Tensor, 
     if slots is not None:
         _need(slots, "slots", i32, (B, slots.shape[1]) if slots.dim() == 2 else (B, -1))
     _same_device(seq_len, block_table, add_len, free_pages, free_count, seq_len_out, free_count_out, slots, err)
+    if B == 0:
+        _same_count(free_count_out, free_count, stream)
     _check(lib().basiskv_assign_pages(cfg._ref(), B, max_pages, min(free_pages.numel(), _I32), _ptr(seq_len),
                                       _ptr(add_len), _ptr(block_table), _ptr(free_pages), _ptr(free_count),
                                       _ptr(seq_len_out), _ptr(free_count_out), _ptr(slots),
@@ -456,6 +465,8 @@ def release_pages(cfg: Config, block_table: torch.Tensor, seq_len: torch.Tensor,
     _need(free_count_out, "free_count_out", i32, (1,))
     _need(err, "err", i32)
     _same_device(seq_len, block_table, release, free_pages, free_count, seq_len_out, free_count_out, err)
+    if B == 0:
+        _same_count(free_count_out, free_count, stream)
     _check(lib().basiskv_release_pages(cfg._ref(), B, max_pages, min(free_pages.numel(), _I32), _ptr(seq_len),
                                        _ptr(release), _ptr(block_table), _ptr(free_pages), _ptr(free_count),
                                        _ptr(seq_len_out), _ptr(free_count_out), _ptr(err), _stream(stream)),
