@@ -423,27 +423,29 @@ def assign_pages(cfg: Config, block_table: torch.Tensor, seq_len: torch.Tensor, 
     from the free list (free_pages [num_phys], its first free_count[0] entries), seq_len_out = seq_len +
     add_len, free_count_out, and (slots [B, cols], or None) the slot page * P + position % P of each new
     token.  seq_len_out may be seq_len and free_count_out may be free_count (basiskv_assign_pages)."""
-    i32, B = torch.int32, seq_len.numel()
+    i32, B, pages = torch.int32, seq_len.numel(), free_pages.numel()
     if block_table.dim() != 2:
         raise ValueError("block_table must be [batch, max_pages]")
     max_pages = block_table.shape[1]
     _need(seq_len, "seq_len", i32, (B,))
     _need(block_table, "block_table", i32, (B, max_pages))
     _need(add_len, "add_len", i32, (B,))
-    _need(free_pages, "free_pages", i32, (free_pages.numel(),))
+    _need(free_pages, "free_pages", i32, (pages,))
     _need(free_count, "free_count", i32, (1,))
     _need(seq_len_out, "seq_len_out", i32, (B,))
     _need(free_count_out, "free_count_out", i32, (1,))
     _need(err, "err", i32)
+    cols = 0
     if slots is not None:
-        _need(slots, "slots", i32, (B, slots.shape[1]) if slots.dim() == 2 else (B, -1))
+        cols = slots.shape[1] if slots.dim() == 2 else -1
+        _need(slots, "slots", i32, (B, cols))
     _same_device(seq_len, block_table, add_len, free_pages, free_count, seq_len_out, free_count_out, slots, err)
     if B == 0:
         _same_count(free_count_out, free_count, stream)
-    _check(lib().basiskv_assign_pages(cfg._ref(), B, max_pages, min(free_pages.numel(), _I32), _ptr(seq_len),
+    _check(lib().basiskv_assign_pages(cfg._ref(), B, max_pages, pages if pages <= _I32 else _I32, _ptr(seq_len),
                                       _ptr(add_len), _ptr(block_table), _ptr(free_pages), _ptr(free_count),
                                       _ptr(seq_len_out), _ptr(free_count_out), _ptr(slots),
-                                      0 if slots is None else min(slots.shape[1], _I32), _ptr(err), _stream(stream)),
+                                      cols if cols <= _I32 else _I32, _ptr(err), _stream(stream)),
            "basiskv_assign_pages")
 
 
@@ -452,14 +454,14 @@ def release_pages(cfg: Config, block_table: torch.Tensor, seq_len: torch.Tensor,
                   free_count_out: torch.Tensor, err: torch.Tensor, stream=None):
     """Back to the free list with the pages of every request whose release[b] is not zero;
     seq_len_out is 0 for them (basiskv_release_pages)."""
-    i32, B = torch.int32, seq_len.numel()
+    i32, B, pages = torch.int32, seq_len.numel(), free_pages.numel()
     if block_table.dim() != 2:
         raise ValueError("block_table must be [batch, max_pages]")
     max_pages = block_table.shape[1]
     _need(seq_len, "seq_len", i32, (B,))
     _need(block_table, "block_table", i32, (B, max_pages))
     _need(release, "release", i32, (B,))
-    _need(free_pages, "free_pages", i32, (free_pages.numel(),))
+    _need(free_pages, "free_pages", i32, (pages,))
     _need(free_count, "free_count", i32, (1,))
     _need(seq_len_out, "seq_len_out", i32, (B,))
     _need(free_count_out, "free_count_out", i32, (1,))
@@ -467,7 +469,7 @@ def release_pages(cfg: Config, block_table: torch.Tensor, seq_len: torch.Tensor,
     _same_device(seq_len, block_table, release, free_pages, free_count, seq_len_out, free_count_out, err)
     if B == 0:
         _same_count(free_count_out, free_count, stream)
-    _check(lib().basiskv_release_pages(cfg._ref(), B, max_pages, min(free_pages.numel(), _I32), _ptr(seq_len),
+    _check(lib().basiskv_release_pages(cfg._ref(), B, max_pages, pages if pages <= _I32 else _I32, _ptr(seq_len),
                                        _ptr(release), _ptr(block_table), _ptr(free_pages), _ptr(free_count),
                                        _ptr(seq_len_out), _ptr(free_count_out), _ptr(err), _stream(stream)),
            "basiskv_release_pages")
