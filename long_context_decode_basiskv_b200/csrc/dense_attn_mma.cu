@@ -17,10 +17,12 @@
 // than 2^8: most tiles need no reduction across the lanes and no rescaling.
 //
 // Measured (bf16, d 128, rank 64, 8 KV heads, 4 heads each): 131 us for 8
-// sequences of 32 k (805 MB, 6.1 TB/s), 141 us for 64 ragged ones with a window
-// and capped scores (806 MB, 5.7 TB/s).  With the rows as M (half of it padding)
+// sequences of 32 k (805 MB, 6.1 TB/s), 139 us for 64 ragged ones with a window
+// and capped scores (806 MB, 5.8 TB/s); 3 and 4 tokens of 8 sequences of 16 k, 12
+// and 16 rows, 82 and 84 us (403 MB).  With the rows as M (half of it padding)
 // the first took 133 us and 138 us against 136 in a loop of calls; at 16 rows,
-// where nothing is padding, that layout is 4% the faster one.  Six warps a CTA,
+// where nothing is padding, that layout is 4% the faster one, and it does not
+// spill (ranks 48 to 96 do here, at the 128 registers of two CTAs an SM).  Six warps a CTA,
 // for more registers and a deeper ring, cost a single sequence of 8 k 20 us
 // instead of 14: its runs no longer end where the sequence's heads do.
 //

@@ -14,10 +14,12 @@
 // fault bits to the others, so a call that cannot be met in full changes
 // nothing.
 //
-// Measured (64 requests, pages of 16): 4.1 us for a token each, 13.7 us for
-// prompts of 2048 to 32768 tokens (69 k table entries, 2.1 M slots written),
-// 11.3 us for the release of half of them.  Bound by the latency of a chain of
-// dependent loads: lengths, free count, page ids, then the stores.  A cluster of
+// Measured (64 requests, pages of 16): 3.8 us for a token each, 13.6 us for
+// prompts of 2048 to 32768 tokens (69 k table entries, 2.1 M slots written; the
+// first kernel takes two thirds of it), 11.2 us for the release of half of them.
+// Bound by the latency of a chain of dependent loads: lengths, free count, page
+// ids, then the stores.  Where entries are many, the ids are read twice (checked,
+// then moved) and each entry looks for its request by bisection.  A cluster of
 // 16 CTAs (beyond the portable size) took 11.3 and 8.6 us for the last two; it
 // is not used, since a device partitioned for others may not offer it.
 #include "kernels.cuh"
