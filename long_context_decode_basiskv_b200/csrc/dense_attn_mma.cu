@@ -21,10 +21,10 @@
 // and capped scores (806 MB, 5.8 TB/s); 3 and 4 tokens of 8 sequences of 16 k, 12
 // and 16 rows, 82 and 84 us (403 MB).  With the rows as M (half of it padding)
 // the first took 133 us and 138 us against 136 in a loop of calls; at 16 rows,
-// where nothing is padding, that layout is 4% the faster one, and it does not
-// spill (ranks 48 to 96 do here, at the 128 registers of two CTAs an SM).  Six warps a CTA,
-// for more registers and a deeper ring, cost a single sequence of 8 k 20 us
-// instead of 14: its runs no longer end where the sequence's heads do.
+// where nothing is padding, that layout is 4% the faster one (ranks 48 to 96
+// spill in both, at the 128 registers of two CTAs an SM).  Six warps a CTA, for
+// more registers and a deeper ring, cost a single sequence of 8 k 20 us instead
+// of 14: its runs no longer end where the sequence's heads do.
 //
 // Where a run ends inside a sequence, the warp leaves (max, sum, acc) in its
 // slot: run w and group g meet in slot w + g, since along the tiles each step

@@ -39,11 +39,11 @@
 // which the exponentials alone are 2048 (16 a cycle) and the MMAs, beside them,
 // 2112.  Measured (bf16, d 128): a prompt of 8192 tokens, 32 heads over 8, rank
 // 64, 582 us (708 TFLOP/s, P C counted once: 0.43 of the measured peak; 626 once
-// the power cap holds the clocks down); 1021
-// tokens after 15360 others, 64 heads over 8, rank 96, capped scores, 1241 us
-// (378 TFLOP/s, the tanh beside the exponentials).  One S tile for each of the
-// two warpgroups took 704 us for the first; three warpgroups of 128 rows 597,
-// and a prompt of 2048 tokens 68 instead of 59.
+// the power cap holds the clocks down); 1021 tokens after 15360 others, 64 heads
+// over 8, rank 96, capped scores, 1241 us (378 TFLOP/s, the tanh beside the
+// exponentials).  One S tile for each of the two warpgroups took 704 us for the
+// first; three warpgroups of 128 rows 597, and a prompt of 2048 tokens 68 instead
+// of 58.
 #include <cuda.h>
 
 #include <algorithm>
